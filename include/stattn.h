@@ -268,6 +268,126 @@ st_status ulysses_relayout_rope(st_relayout_mode mode, const void *in, void *out
                                 int rope_positions, st_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Conditioning: the block's attention to what its samples are conditioned on
+ * (a text encoder's states, reference frames), and the norms of the queries
+ * and keys where no relayout takes place [xD section 4.1.1: condition and
+ * image sequences; CC "V-First": RMSNorm and RoPE on Q and K].  The pages
+ * print no formula or API for these; the readings are stated here.
+ * ---------------------------------------------------------------------- */
+
+/* Which channels of a head turn together: ST_ROPE_INTERLEAVED pairs channel
+ * 2i with 2i + 1 (as ulysses_relayout_rope does), ST_ROPE_HALVES pairs i with
+ * i + D/2.  Pair i turns by entry i of the token's table row in both. */
+typedef enum { ST_ROPE_INTERLEAVED = 0, ST_ROPE_HALVES = 1 } st_rope_pairing;
+
+/* Q is n_tokens rows of h_q heads, K n_tokens rows of h_k heads, each head D
+ * channels: element (n, h, d) of Q lies at n*stride_q + h*D + d, of K at
+ * n*stride_k + h*D + d, and the outputs likewise.  Zero strides mean dense
+ * rows; strides of a fused projection address its Q and K in place.
+ * h_q or h_k may be 0 (that tensor is absent). */
+typedef struct {
+  int size;               /* sizeof(st_qk_desc)                                 */
+  int n_tokens, h_q, h_k, D;   /* D a multiple of 8, at most 256                */
+  st_dtype dtype;         /* of Q, K and both outputs                           */
+  float eps;              /* >= 0                                               */
+  int pairing;            /* st_rope_pairing                                    */
+  int pos_period;         /* without positions: token n is at n % pos_period
+                             (0: at n), its index in the attended sequence      */
+  long long stride_q, stride_k, stride_q_out, stride_k_out;   /* elements between
+                             tokens; 0 -> dense                                 */
+} st_qk_desc;
+
+/* Per-head RMSNorm of Q and K and their rotary embedding in one pass:
+ *   y = x / sqrt(mean_d(x^2) + eps) * gamma[d];  then every pair (a, b) of y
+ *   becomes (a cos - b sin, a sin + b cos) with (cos, sin) = rope_table[pos][i].
+ *   q_gamma, k_gamma: fp32 device [D], shared by the heads; NULL means 1.
+ *   rope_table: fp32 device [rope_positions][D / 2][2] (st_rope_table), 16-byte
+ *     aligned, or NULL for no rotation.  Any scheme of angles (several axes,
+ *     scaled positions) is a table: row p is turned as the caller filled it.
+ *   positions: optional int32 device [n_tokens].  A position outside
+ *     [0, rope_positions) leaves that token's heads normalised and unrotated
+ *     (condition tokens of a joint sequence carry none).  Without positions
+ *     the table must hold min(n_tokens, pos_period) rows.
+ *   An output may be its input (same pointer and stride, in place); any other
+ *   overlap of an output with an input or the other output is ST_ERR_SHAPE
+ *   (Q and K as columns of the same rows do not overlap).  Pointers and
+ *   strides must be multiples of 16 bytes (ST_ERR_ALIGN).  Sums in fp32, one
+ *   rounding to dtype.  ST_ERR_UNSUPPORTED for another D. */
+st_status st_qk_norm_rope(const st_qk_desc *desc, const void *q, const void *k, void *q_out,
+                          void *k_out, const float *q_gamma, const float *k_gamma,
+                          const float *rope_table, int rope_positions, const int *positions,
+                          st_stream_t stream);
+
+/* Keys and values of another length than the queries': n_sets sequences of L
+ * rows of H_kv heads.  Batch b of B attends set b / (B / n_sets), so samples
+ * that share their states share one copy; query head h reads head
+ * h / (H / H_kv).  Element (set, l, h, d) of K and of V lies at
+ * set*stride_set + l*stride_l + h*D + d.
+ *   len: optional int32 device [n_sets], keys of each set (clamped to [0, L]).
+ *   offsets: optional int32 device [n_sets + 1]: the sets are packed one
+ *     behind the other, set i in rows [offsets[i], offsets[i + 1]) of n_rows
+ *     rows (row r at r*stride_l), at most L of them counted; offsets are
+ *     clamped to [0, n_rows].  Excludes len and mask.
+ *   mask: optional u8 device [n_sets, L] dense, nonzero = the key counts.
+ * Keys that do not count may hold anything, NaN and infinities included.
+ * Rows of a mask's tail cost time; give len too where the tail is long. */
+typedef struct {
+  int size;               /* sizeof(st_kv_desc)                                 */
+  int n_sets, L;          /* n_sets divides B; L >= 1 (0 only with len NULL,
+                             offsets NULL, mask NULL: no keys)                  */
+  int H_kv;               /* divides H; 0 -> H                                  */
+  long long stride_set, stride_l;   /* elements; 0 -> dense                     */
+  long long n_rows;       /* packed: rows of K and V                            */
+  const int *len;
+  const int *offsets;
+  const unsigned char *mask;
+} st_kv_desc;
+
+/* Cross attention: for every (b, t, s, h)
+ *     O[b,t,s,h,:] = softmax_l(Q[b,t,s,h,:] . K[set(b),l,h',:] * scale) V[set(b),l,h',:]
+ * over the keys l of the batch's set that count.  No such key: O = 0 and
+ * lse = -inf.
+ *   desc: Q and O as in st_attn_spatial (their strides only; T frames of S
+ *     queries, T = S = 1 for a single query); kv_begin, kv_end must be 0 and
+ *     slices are not taken (ST_ERR_UNSUPPORTED).  o_fp32 writes an fp32 partial
+ *     that st_attn_spatial_merge and attn_chunk_merge take with its lse.
+ *   lse: optional fp32 [B, T, H, S] dense.
+ *   workspace: device memory of st_attn_cross_workspace_bytes bytes, 16-byte
+ *     aligned.  It is asked for (the size is not 0) when there are too few
+ *     queries to fill the GPU and the keys are split over it; nothing is kept in
+ *     it between calls.  NULL: not split (the same result up to rounding
+ *     order, slower).  Calls that may run at the same time need one each.
+ *   o must not overlap an input or the workspace.
+ *   bf16 runs on the tcgen05 tensor cores, fp32 on the FMA pipes, both with fp32
+ *   statistics and accumulation.  Errors as st_attn_spatial; ST_ERR_SHAPE for
+ *   a bad st_kv_desc or a short workspace, ST_ERR_DIVISIBILITY when n_sets or
+ *   H_kv does not divide. */
+st_status st_attn_cross(const st_attn_desc *desc, const st_kv_desc *kv, const void *q, const void *k,
+                        const void *v, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                        st_stream_t stream);
+/* Bytes of workspace for that call on the current device; 0: none needed (or
+ * bad arguments, which the call itself reports).  Depends on sizes, dtype and
+ * strides only. */
+size_t st_attn_cross_workspace_bytes(const st_attn_desc *desc, const st_kv_desc *kv);
+
+/* Attention behind a shared prefix: the keys of batch b are those of its
+ * prefix set (condition tokens or reference frames held once for the B /
+ * prefix->n_sets samples that share them), followed by those of its own set:
+ *     O = softmax over [K_prefix[set_p(b)]; K[set(b)]] . [V_prefix; V]
+ * without laying the two behind one another.  With own->n_sets = B and the
+ * samples' own tokens as queries it is in-context-conditioned (joint)
+ * self-attention.  Where each sample has few queries, those that share a
+ * prefix attend to it together (with a workspace), so the prefix is read once
+ * for all.  Arguments, results and errors as st_attn_cross; both descriptors
+ * may use len, offsets or mask, H_kv must be the same (ST_ERR_SHAPE). */
+st_status st_attn_prefix(const st_attn_desc *desc, const st_kv_desc *prefix, const st_kv_desc *own,
+                         const void *q, const void *k_prefix, const void *v_prefix, const void *k,
+                         const void *v, void *o, float *lse, void *workspace,
+                         size_t workspace_bytes, st_stream_t stream);
+size_t st_attn_prefix_workspace_bytes(const st_attn_desc *desc, const st_kv_desc *prefix,
+                                      const st_kv_desc *own);
+
+/* ------------------------------------------------------------------------
  * V-Major selective communication [CC "V-Major"].
  * ---------------------------------------------------------------------- */
 

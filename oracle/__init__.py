@@ -29,10 +29,14 @@ Every function restates, in float64 numpy, what the pages define:
 * vmajor      -- per-token L1 change of V against the previous step, the
                  threshold mask, the ascending list of active tokens and the
                  cache update (CoCoDiff article, "V-Major" section).
+* conditioning -- the norms and the rotation where no relayout takes place,
+                 attention to states of another length (cross attention) and
+                 behind a shared prefix.
 
 Each pin of these functions lives in ``tests/test_oracle_*.py``.
 """
 from .attention import attention, spatial, temporal, merge_chunks, frames_view
+from .conditioning import conditioned, qk_norm_rope
 from .relayout import (st_x_rows, st_y_rows, st_relayout, seq_head_relayout,
                        st_logical_from_x, st_logical_from_y, st_row_pairs, seq_head_row_pairs)
 from .rmsnorm import rmsnorm_heads
@@ -41,6 +45,7 @@ from .vmajor import l1_change, change_mask, compact, scatter_rows, pack_rows, ta
 
 __all__ = [
     "attention", "spatial", "temporal", "merge_chunks", "frames_view",
+    "conditioned", "qk_norm_rope",
     "st_x_rows", "st_y_rows", "st_relayout", "seq_head_relayout",
     "st_logical_from_x", "st_logical_from_y", "st_row_pairs", "seq_head_row_pairs",
     "rmsnorm_heads", "rope_angles", "rope_table", "rope_heads",

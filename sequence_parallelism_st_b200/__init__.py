@@ -10,6 +10,7 @@ Entry points (same names as the C ABI in include/stattn.h):
     ulysses_relayout_range, vmajor_mask_compact, vmajor_mask_compact_noalloc, vmajor_mask_compact_scatter,
     vmajor_scatter_rows, vmajor_workspace_bytes, vmajor_relayout_mask, vmajor_relayout_rows,
     st_rope_table, ulysses_relayout_rope,
+    st_qk_norm_rope, st_attn_cross, st_attn_cross_workspace_bytes, st_attn_prefix, st_attn_prefix_workspace_bytes,
     st_check_device_status, st_status_string, st_set_sm_budget, st_get_sm_budget
 """
 from __future__ import annotations
@@ -32,6 +33,8 @@ ST_OK, ST_ERR_NULL, ST_ERR_SHAPE, ST_ERR_DIVISIBILITY, ST_ERR_DTYPE = 0, -1, -2,
 ST_ERR_ALIGN, ST_ERR_UNSUPPORTED, ST_ERR_CUDA, ST_ERR_TIMEOUT = -5, -6, -7, -8
 ST_F32, ST_BF16 = 0, 1
 ST_S2T, ST_T2S, ST_SEQ2HEAD, ST_HEAD2SEQ = 0, 1, 2, 3
+ST_ROPE_INTERLEAVED, ST_ROPE_HALVES = 0, 1
+PAIRINGS = {"interleaved": ST_ROPE_INTERLEAVED, "halves": ST_ROPE_HALVES}
 MODES = {"S2T": ST_S2T, "T2S": ST_T2S, "SEQ2HEAD": ST_SEQ2HEAD, "HEAD2SEQ": ST_HEAD2SEQ}
 
 c_int, c_ll, c_float, c_void_p, c_size_t = (ctypes.c_int, ctypes.c_longlong, ctypes.c_float,
@@ -45,6 +48,17 @@ class st_attn_desc(ctypes.Structure):
                 ("t_block", c_int), ("stride_tb", c_ll), ("s_block", c_int), ("stride_sb", c_ll),
                 ("n_slices", c_int), ("slice", c_int), ("kv_begin", c_int), ("kv_end", c_int),
                 ("o_fp32", c_int)]
+
+
+class st_qk_desc(ctypes.Structure):
+    _fields_ = [("size", c_int), ("n_tokens", c_int), ("h_q", c_int), ("h_k", c_int), ("D", c_int),
+                ("dtype", c_int), ("eps", c_float), ("pairing", c_int), ("pos_period", c_int),
+                ("stride_q", c_ll), ("stride_k", c_ll), ("stride_q_out", c_ll), ("stride_k_out", c_ll)]
+
+
+class st_kv_desc(ctypes.Structure):
+    _fields_ = [("size", c_int), ("n_sets", c_int), ("L", c_int), ("H_kv", c_int), ("stride_set", c_ll),
+                ("stride_l", c_ll), ("n_rows", c_ll), ("len", c_void_p), ("offsets", c_void_p), ("mask", c_void_p)]
 
 
 def _proto(name, res, *args):
@@ -92,6 +106,16 @@ _c = {
     "ulysses_relayout_rope": _proto("ulysses_relayout_rope", c_int, c_int, _VP, _VP, c_int, c_int, c_int, c_int,
                                     c_int, c_int, c_int, c_int, _VP, c_int, c_float, _VP, c_int, _VP),
     "st_get_sm_budget": _proto("st_get_sm_budget", c_int),
+    "st_qk_norm_rope": _proto("st_qk_norm_rope", c_int, ctypes.POINTER(st_qk_desc), _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                              c_int, _VP, _VP),
+    "st_attn_cross": _proto("st_attn_cross", c_int, ctypes.POINTER(st_attn_desc), ctypes.POINTER(st_kv_desc), _VP, _VP,
+                            _VP, _VP, _VP, _VP, c_size_t, _VP),
+    "st_attn_cross_workspace_bytes": _proto("st_attn_cross_workspace_bytes", c_size_t, ctypes.POINTER(st_attn_desc),
+                                            ctypes.POINTER(st_kv_desc)),
+    "st_attn_prefix": _proto("st_attn_prefix", c_int, ctypes.POINTER(st_attn_desc), ctypes.POINTER(st_kv_desc),
+                             ctypes.POINTER(st_kv_desc), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, c_size_t, _VP),
+    "st_attn_prefix_workspace_bytes": _proto("st_attn_prefix_workspace_bytes", c_size_t, ctypes.POINTER(st_attn_desc),
+                                             ctypes.POINTER(st_kv_desc), ctypes.POINTER(st_kv_desc)),
 }
 
 EXPORTED = ["st_status_string", "st_abi_version", "st_attn_spatial", "st_attn_ring", "st_attn_spatial_merge",
@@ -101,7 +125,8 @@ EXPORTED = ["st_status_string", "st_abi_version", "st_attn_spatial", "st_attn_ri
             "vmajor_scatter_rows", "vmajor_mask_compact_scatter",
             "st_check_device_status", "st_selftest_wait_timeout", "ulysses_relayout_range", "st_set_sm_budget",
             "st_get_sm_budget", "vmajor_relayout_mask", "vmajor_relayout_rows", "st_rope_table",
-            "ulysses_relayout_rope", "st_selftest_ex2"]
+            "ulysses_relayout_rope", "st_selftest_ex2", "st_qk_norm_rope", "st_attn_cross", "st_attn_cross_workspace_bytes",
+            "st_attn_prefix", "st_attn_prefix_workspace_bytes"]
 
 
 class StattnError(RuntimeError):
@@ -322,6 +347,229 @@ def ulysses_relayout_rope(mode, inp, out, P, B, T_or_N, S_or_H, C_or_D, n_t=1, n
                                     n_s, _ptr(rms_gamma), int(rms_head_dim), float(rms_eps), _ptr(rope_table), n_pos,
                                     _stream(stream))
     return r if raw else _check(r, "ulysses_relayout_rope")
+
+
+# ---------------------------------------------------------------- conditioning
+def _device_call(where, fn, device, stream, *args):
+    """fn(*args, stream) with ``device`` current, on ``stream`` or the device's current stream."""
+    import torch
+    if device.type != "cuda":
+        raise StattnError(ST_ERR_NULL, f"{where}: tensors must be on a CUDA device")
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(stream))
+
+
+def _expect(ok, code, what):
+    if not ok:
+        raise StattnError(code, what)
+
+
+def _same_device(where, device, *tensors):
+    for t in tensors:
+        _expect(t is None or t.device == device, ST_ERR_SHAPE, f"{where}: tensors on different devices")
+
+
+def _int32(where, t, n, device):
+    """Pointer of an optional contiguous int32 tensor of n elements."""
+    if t is None:
+        return None
+    import torch
+    _expect(t.dtype == torch.int32, ST_ERR_DTYPE, f"{where}: lengths, offsets and positions are int32")
+    _expect(t.numel() == n and t.is_contiguous() and t.device == device, ST_ERR_SHAPE,
+            f"{where}: {n} contiguous int32 on the tensors' device expected")
+    return t.data_ptr()
+
+
+def _rows(where, t):
+    """(tokens, H, D, elements between tokens) of a [..., H, D] tensor whose tokens have one stride."""
+    _expect(t.dim() >= 3, ST_ERR_SHAPE, f"{where}: [..., H, D] expected")
+    size, stride = t.shape, t.stride()
+    H, D = size[-2], size[-1]
+    _expect((D == 1 or stride[-1] == 1) and (H == 1 or stride[-2] == D), ST_ERR_SHAPE, f"{where}: heads must be dense")
+    n, step = 1, 0
+    for i in range(len(size) - 3, -1, -1):
+        if size[i] == 1:
+            continue
+        _expect(n == 1 or stride[i] == n * step, ST_ERR_SHAPE, f"{where}: tokens must have one stride")
+        if n == 1:
+            step = stride[i]
+            _expect(step > 0, ST_ERR_SHAPE, f"{where}: expanded tensors are not taken")
+        n *= size[i]
+    return n, H, D, step
+
+
+def st_qk_norm_rope(q, k=None, q_out=None, k_out=None, q_gamma=None, k_gamma=None, eps=1e-6, *, rope_table=None,
+                    positions=None, pos_period=0, pairing="interleaved", stream=None, raw=False):
+    """Per-head RMSNorm of Q and K and their rotary embedding in one pass (include/stattn.h).
+
+    q, k: [..., H, D] with one stride between tokens (views of a fused projection
+    included); either may be None.  Outputs default to in place."""
+    import torch
+    x = q if q is not None else k
+    _expect(x is not None, ST_ERR_NULL, "st_qk_norm_rope: q or k")
+    d = st_qk_desc(size=ctypes.sizeof(st_qk_desc), dtype=_dtype_code(x), eps=float(eps), pos_period=int(pos_period),
+                   pairing=PAIRINGS[pairing] if isinstance(pairing, str) else int(pairing))
+    for name, t, out, gamma in (("q", q, q_out, q_gamma), ("k", k, k_out, k_gamma)):
+        if t is None:
+            _expect(out is None, ST_ERR_NULL, f"st_qk_norm_rope: {name}_out without {name}")
+            continue
+        n, H, D, step = _rows("st_qk_norm_rope", t)
+        _expect(d.n_tokens in (0, n) and d.D in (0, D), ST_ERR_SHAPE, "st_qk_norm_rope: q and k differ in tokens or D")
+        d.n_tokens, d.D = n, D
+        setattr(d, "h_" + name, H)
+        setattr(d, "stride_" + name, step)
+        if out is not None:
+            _expect(out.shape == t.shape, ST_ERR_SHAPE, f"st_qk_norm_rope: {name}_out has another shape")
+            step = _rows("st_qk_norm_rope", out)[3]
+        setattr(d, f"stride_{name}_out", step)
+        _same_device("st_qk_norm_rope", x.device, t, out, gamma)
+        _expect(t.dtype == x.dtype and (out is None or out.dtype == x.dtype), ST_ERR_DTYPE,
+                "st_qk_norm_rope: one dtype for q, k and the outputs")
+        _expect(gamma is None or (gamma.dtype == torch.float32 and gamma.numel() == D and gamma.is_contiguous()),
+                ST_ERR_SHAPE, f"st_qk_norm_rope: {name}_gamma is fp32 [D]")
+    n_pos = 0
+    if rope_table is not None:
+        _same_device("st_qk_norm_rope", x.device, rope_table)
+        n_pos = rope_table.shape[0]
+        _expect(rope_table.dtype == torch.float32 and rope_table.is_contiguous() and
+                rope_table.numel() == n_pos * d.D, ST_ERR_SHAPE, "st_qk_norm_rope: rope_table is fp32 [n, D / 2, 2]")
+    pos = _int32("st_qk_norm_rope", positions, d.n_tokens, x.device)
+    r = _device_call("st_qk_norm_rope", _c["st_qk_norm_rope"], x.device, stream, ctypes.byref(d), _ptr(q), _ptr(k),
+                     _ptr(q if q_out is None else q_out), _ptr(k if k_out is None else k_out), _ptr(q_gamma),
+                     _ptr(k_gamma), _ptr(rope_table), n_pos, pos)
+    return r if raw else _check(r, "st_qk_norm_rope")
+
+
+def _q_desc(where, q, o, kw):
+    """Descriptor of Q and O [B, T, S, H, D], strides taken from the tensors."""
+    _expect(q.dim() == 5, ST_ERR_SHAPE, f"{where}: q is [B, T, S, H, D]")
+    B, T, S, H, D = q.shape
+    for t in (q, o):
+        if t is None:
+            continue
+        st = t.stride()
+        _expect(t.shape == q.shape and (D == 1 or st[4] == 1) and (H == 1 or st[3] == D), ST_ERR_SHAPE,
+                f"{where}: q and o are [B, T, S, H, D] with dense heads")
+        _expect(all(n == 1 or (a > 0 and a == b) for n, a, b in zip(q.shape[:3], st, q.stride())), ST_ERR_SHAPE,
+                f"{where}: q and o need the same strides")
+    sb, ss, stt = (q.stride(i) if q.shape[i] > 1 else 0 for i in (0, 2, 1))
+    if T > 1 and stt == S * (ss or H * D):
+        stt = 0                                 # dense frames
+    return make_desc(B, T, S, H, D, _dtype_code(q), stride_b=sb, stride_t=stt, stride_s=ss, **kw)
+
+
+def _kv_desc(where, head_dim, q, k, v, length, offsets, mask, max_len):
+    """st_kv_desc of K (and V) [n_sets, L, H_kv, D], or packed [rows, H_kv, D] with offsets."""
+    import torch
+    packed = offsets is not None
+    _expect(k.dim() == (3 if packed else 4), ST_ERR_SHAPE,
+            f"{where}: keys are [n_sets, L, H_kv, D], or [rows, H_kv, D] with offsets")
+    H, D = k.shape[-2:]
+    L = k.shape[-3]
+    st = k.stride()
+    _expect(D == head_dim and (D == 1 or st[-1] == 1) and (H == 1 or st[-2] == D), ST_ERR_SHAPE,
+            f"{where}: keys need q's head dim and dense heads")
+    _expect(k.dtype == q.dtype and (v is None or v.dtype == q.dtype), ST_ERR_DTYPE, f"{where}: one dtype for q, k and v")
+    if v is not None:
+        _expect(v.shape == k.shape and all(n == 1 or a == b for n, a, b in zip(k.shape, st, v.stride())),
+                ST_ERR_SHAPE, f"{where}: k and v need the same shape and strides")
+    _same_device(where, q.device, k, v, length, offsets, mask)
+    _expect(L <= 1 or st[-3] > 0, ST_ERR_SHAPE, f"{where}: expanded tensors are not taken")
+    sl = st[-3] if L > 1 else 0
+    d = st_kv_desc(size=ctypes.sizeof(st_kv_desc), L=L, H_kv=H, stride_l=sl)
+    if packed:
+        _expect(length is None and mask is None, ST_ERR_SHAPE, f"{where}: offsets exclude lengths and mask")
+        d.n_sets, d.n_rows = offsets.numel() - 1, L
+        d.L = int(max_len) if max_len is not None else L
+        d.offsets = _int32(where, offsets, d.n_sets + 1, q.device)
+    else:
+        d.n_sets = k.shape[0]
+        if d.n_sets > 1:
+            _expect(st[0] > 0, ST_ERR_SHAPE, f"{where}: expanded tensors are not taken")
+            d.stride_set = st[0]
+        d.len = _int32(where, length, d.n_sets, q.device)
+        if mask is not None:
+            _expect(mask.dtype in (torch.uint8, torch.bool), ST_ERR_DTYPE, f"{where}: the mask is uint8 or bool")
+            _expect(mask.shape == k.shape[:2] and mask.is_contiguous(), ST_ERR_SHAPE, f"{where}: the mask is [n_sets, L]")
+            d.mask = mask.data_ptr()
+    return d
+
+
+def _workspace(where, t, device):
+    if t is None or t.numel() == 0:
+        return None, 0
+    _expect(t.device == device and t.is_contiguous(), ST_ERR_SHAPE, f"{where}: workspace")
+    return _ptr(t), t.numel() * t.element_size()
+
+
+def _check_out(where, q, o, lse, o_fp32):
+    import torch
+    _expect(o.dtype == (torch.float32 if o_fp32 else q.dtype), ST_ERR_DTYPE, f"{where}: o's dtype")
+    _same_device(where, q.device, o, lse)
+    if lse is not None:
+        B, T, S, H, _ = q.shape
+        _expect(lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == B * T * H * S, ST_ERR_SHAPE,
+                f"{where}: lse is fp32 [B, T, H, S]")
+
+
+def st_attn_cross(q, k, v, o, lse=None, *, kv_len=None, kv_offsets=None, kv_mask=None, max_len=None, workspace=None,
+                  desc: st_attn_desc | None = None, stream=None, raw=False, **kw):
+    """Cross attention of Q [B, T, S, H, D] to K, V [n_sets, L, H_kv, D] (include/stattn.h).
+
+    With ``kv_offsets`` [n_sets + 1], K and V are packed [rows, H_kv, D], at most
+    ``max_len`` rows of a set counted.  Strides come from the tensors (Q and O
+    alike); ``desc`` overrides Q's.  ``workspace``: st_attn_cross_workspace_bytes
+    bytes."""
+    if desc is None:
+        desc = _q_desc("st_attn_cross", q, o, kw)
+        _check_out("st_attn_cross", q, o, lse, desc.o_fp32)
+    kv = _kv_desc("st_attn_cross", desc.D, q, k, v, kv_len, kv_offsets, kv_mask, max_len)
+    ws, n = _workspace("st_attn_cross", workspace, q.device)
+    r = _device_call("st_attn_cross", _c["st_attn_cross"], q.device, stream, ctypes.byref(desc), ctypes.byref(kv),
+                     _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), ws, n)
+    return r if raw else _check(r, "st_attn_cross")
+
+
+def st_attn_cross_workspace_bytes(q, k, *, kv_len=None, kv_offsets=None, kv_mask=None, max_len=None,
+                                  desc: st_attn_desc | None = None, **kw) -> int:
+    """Bytes of workspace st_attn_cross asks for with these arguments (0: none)."""
+    desc = desc if desc is not None else _q_desc("st_attn_cross_workspace_bytes", q, None, kw)
+    kv = _kv_desc("st_attn_cross_workspace_bytes", desc.D, q, k, None, kv_len, kv_offsets, kv_mask, max_len)
+    import torch
+    with torch.cuda.device(q.device):
+        return int(_c["st_attn_cross_workspace_bytes"](ctypes.byref(desc), ctypes.byref(kv)))
+
+
+def st_attn_prefix(q, k_prefix, v_prefix, k, v, o, lse=None, *, prefix_len=None, prefix_offsets=None,
+                   prefix_mask=None, prefix_max_len=None, kv_len=None, kv_offsets=None, kv_mask=None, max_len=None,
+                   workspace=None, desc: st_attn_desc | None = None, stream=None, raw=False, **kw):
+    """Attention of Q [B, T, S, H, D] over a prefix shared by several batches, then the batch's own keys
+    (include/stattn.h).  Arguments as st_attn_cross, once for the prefix and once for the own keys."""
+    if desc is None:
+        desc = _q_desc("st_attn_prefix", q, o, kw)
+        _check_out("st_attn_prefix", q, o, lse, desc.o_fp32)
+    pre = _kv_desc("st_attn_prefix", desc.D, q, k_prefix, v_prefix, prefix_len, prefix_offsets, prefix_mask, prefix_max_len)
+    kv = _kv_desc("st_attn_prefix", desc.D, q, k, v, kv_len, kv_offsets, kv_mask, max_len)
+    ws, n = _workspace("st_attn_prefix", workspace, q.device)
+    r = _device_call("st_attn_prefix", _c["st_attn_prefix"], q.device, stream, ctypes.byref(desc), ctypes.byref(pre),
+                     ctypes.byref(kv), _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
+                     ws, n)
+    return r if raw else _check(r, "st_attn_prefix")
+
+
+def st_attn_prefix_workspace_bytes(q, k_prefix, k, *, prefix_len=None, prefix_offsets=None, prefix_mask=None,
+                                   prefix_max_len=None, kv_len=None, kv_offsets=None, kv_mask=None, max_len=None,
+                                   desc: st_attn_desc | None = None, **kw) -> int:
+    """Bytes of workspace st_attn_prefix asks for with these arguments (0: none)."""
+    where = "st_attn_prefix_workspace_bytes"
+    desc = desc if desc is not None else _q_desc(where, q, None, kw)
+    pre = _kv_desc(where, desc.D, q, k_prefix, None, prefix_len, prefix_offsets, prefix_mask, prefix_max_len)
+    kv = _kv_desc(where, desc.D, q, k, None, kv_len, kv_offsets, kv_mask, max_len)
+    import torch
+    with torch.cuda.device(q.device):
+        return int(_c["st_attn_prefix_workspace_bytes"](ctypes.byref(desc), ctypes.byref(pre), ctypes.byref(kv)))
 
 
 def st_check_device_status(stream=None) -> int:

@@ -1,0 +1,361 @@
+// st_attn_cross and st_attn_prefix: validation, the plan of a launch, and the
+// kernel that combines split parts.
+//
+// The plan, from sizes and strides alone:
+//   * Frames and tokens with one stride between rows are one unit of T * S
+//     rows, and batches that share their only set of keys and follow one
+//     another in memory are one unit too: full row tiles, one walk over the
+//     shared keys.
+//   * Grouped heads (H > H_kv) of units below one 128-row tile become rows, so
+//     a K/V tile is read once for its whole group.
+//   * Few work items: the keys are split into parts whose fp32 partials go to
+//     the workspace and are combined by a second kernel, as attn_chunk_merge
+//     does (same formula), so that one query over long states still uses every SM.
+//   * Samples of at most PACK_ROWS rows that share a prefix attend to it in
+//     packed tiles; the combine kernel attends each row's own keys.
+#include <math.h>
+
+#include "cond.cuh"
+
+namespace {
+
+using st::CondParams;
+using st::Geom;
+using st::KvSeg;
+
+// Rows per sample (heads of a group included) up to which the samples of a
+// prefix are packed.
+constexpr int PACK_ROWS = 32;
+constexpr int MAX_SPLIT = 64;
+constexpr int MIN_STEPS = 4;   // key steps of a part at least
+
+bool d_supported(int D) { return D == 32 || D == 64 || D == 72 || D == 80 || D == 96 || D == 128; }
+
+st_status make_seg(const st_kv_desc *d, const Geom &g, KvSeg &s, int &H_kv) {
+  if (!d) return ST_ERR_NULL;
+  if (d->size != (int)sizeof(st_kv_desc)) return ST_ERR_SHAPE;
+  if (d->n_sets <= 0 || d->L < 0 || d->H_kv < 0 || d->stride_set < 0 || d->stride_l < 0 || d->n_rows < 0)
+    return ST_ERR_SHAPE;
+  if (d->L == 0 && (d->len || d->offsets || d->mask)) return ST_ERR_SHAPE;
+  if (d->offsets && (d->len || d->mask || d->n_rows > 0x7fffffffLL)) return ST_ERR_SHAPE;
+  if (!d->offsets && d->n_rows) return ST_ERR_SHAPE;
+  if (g.B % d->n_sets) return ST_ERR_DIVISIBILITY;
+  H_kv = d->H_kv ? d->H_kv : g.H;
+  if (g.H % H_kv) return ST_ERR_DIVISIBILITY;
+  s = KvSeg{};
+  s.L = d->L;
+  s.n_sets = d->n_sets;
+  s.per = g.B / d->n_sets;
+  s.len = d->len;
+  s.offsets = d->offsets;
+  s.mask = d->mask;
+  s.n_rows = int(d->n_rows);
+  const long long row = (long long)H_kv * g.D;
+  s.stride_l = d->stride_l ? d->stride_l : row;
+  s.stride_set = d->stride_set ? d->stride_set : (long long)d->L * s.stride_l;
+  if (s.stride_l < row) return ST_ERR_SHAPE;
+  // packed sets of no rows at all: no keys
+  if (d->offsets && d->n_rows == 0) s.L = 0;
+  return ST_OK;
+}
+
+bool seg_aligned(const KvSeg &s, int esize) {
+  return s.stride_l % (16 / esize) == 0 && s.stride_set % (16 / esize) == 0;
+}
+
+struct Plan {
+  CondParams p;
+  st_dtype dtype;
+  size_t workspace;            // bytes asked for; 0: none
+};
+
+int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
+
+// with_ws = false: the plan of a call without workspace.
+st_status make_plan(const st_attn_desc *desc, const st_kv_desc *d0, const st_kv_desc *d1, bool with_ws, Plan &pl) {
+  Geom g;
+  int lo, hi;
+  st_status s = st::make_geom(desc, false, g, lo, hi);
+  if (s != ST_OK) return s;
+  if (desc->kv_begin != 0 || desc->kv_end != 0) return ST_ERR_SHAPE;
+  if (lo != 0 || hi != g.T) return ST_ERR_UNSUPPORTED;
+  const bool bf16 = desc->dtype == ST_BF16;
+  if (bf16 ? !d_supported(g.D) : g.D > 128) return ST_ERR_UNSUPPORTED;
+  if (g.sblk != g.S && g.ssb != (long long)g.sblk * g.ss) return ST_ERR_UNSUPPORTED;
+  if (g.tblk != g.T && g.sb != (long long)(g.T / g.tblk) * g.stb) return ST_ERR_UNSUPPORTED;
+  if (g.ss < (long long)g.H * g.D) return ST_ERR_SHAPE;
+  if (bf16 && (g.ss % 8 || g.st % 8 || g.stb % 8 || g.sb % 8)) return ST_ERR_ALIGN;
+  CondParams &p = pl.p;
+  p = CondParams{};
+  int hk0, hk1;
+  KvSeg seg0, seg1;
+  if ((s = make_seg(d0, g, seg0, hk0)) != ST_OK) return s;
+  if (bf16 && !seg_aligned(seg0, 2)) return ST_ERR_ALIGN;
+  p.seg[0] = seg0;
+  p.n_seg = 1;
+  if (d1) {
+    if ((s = make_seg(d1, g, seg1, hk1)) != ST_OK) return s;
+    if (bf16 && !seg_aligned(seg1, 2)) return ST_ERR_ALIGN;
+    if (hk1 != hk0) return ST_ERR_SHAPE;
+    p.seg[1] = seg1;
+    p.n_seg = 2;
+  }
+  const long long all_rows = (long long)g.B * g.T * g.S;
+  if (all_rows * g.H >= (1LL << 31) || (long long)seg0.L + (d1 ? seg1.L : 0) >= (1LL << 30)) return ST_ERR_SHAPE;
+  p.T0 = g.T;
+  p.S0 = g.S;
+  p.B0 = g.B;
+  p.bm = 1;
+  // one stride between all rows of a batch
+  const bool flat = g.T == 1 || (g.st == (long long)g.S * g.ss && (g.tblk == g.T || g.stb == (long long)g.tblk * g.st));
+  if (flat) {
+    g.S *= g.T;
+    g.T = 1;
+  }
+  g.sblk = g.S;
+  g.ssb = (long long)g.S * g.ss;
+  if (flat) {
+    g.tblk = 1;
+    g.st = g.stb = g.ssb;
+  }
+  const int grp = g.H / hk0;
+  // batches that share every key they attend, or (few rows) their prefix
+  const bool follow = flat && g.sb == (long long)g.S * g.ss;
+  const bool share = !d1 && seg0.per > 1 && follow;
+  const bool pack = with_ws && d1 && seg0.per > 1 && follow && (long long)g.S * grp <= PACK_ROWS;
+  if (share || pack) {
+    p.bm = seg0.per;
+    if (pack) {
+      p.own = seg1;
+      p.n_seg = 1;
+    }
+    g.B /= p.bm;
+    g.sb *= p.bm;
+    g.S *= p.bm;
+    g.sblk = g.S;
+    g.st = g.stb = g.ssb = (long long)g.S * g.ss;
+  }
+  const bool pack_heads = flat && grp > 1 && g.S < 128 && grp <= 128;
+  p.G = pack_heads ? grp : 1;
+  p.HW = g.H / p.G;
+  p.hdiv = pack_heads ? 1 : grp;
+  p.g = g;
+  p.R0 = g.S;
+  p.R = g.S * p.G;
+  p.part_rows = all_rows * g.H;
+  p.scale = desc->scale > 0.f ? desc->scale : 1.0f / sqrtf((float)g.D);
+  p.o_f32 = desc->o_fp32 || !bf16;
+  pl.dtype = desc->dtype;
+  // split the keys when the items leave more than half of the GPU idle
+  const st::CondTile t = bf16 ? st::cond_tile(g.D) : st::CondTile{64, 64};
+  long long steps = 0;
+  for (int i = 0; i < p.n_seg; ++i) steps += ceil_div(p.seg[i].L, t.keys);
+  const long long items = (long long)st::cond_units(p) * p.HW * ceil_div(p.R, t.rows);
+  const long long cap = (long long)st::device_sms() * (bf16 ? 1 : 2);
+  p.n_split = 1;
+  if (with_ws && items * 2 <= cap && steps >= 2 * MIN_STEPS) {
+    long long n = cap / items;
+    if (n > steps / MIN_STEPS) n = steps / MIN_STEPS;
+    p.n_split = int(n > MAX_SPLIT ? MAX_SPLIT : n);
+  }
+  pl.workspace = p.n_split > 1 || pack ? size_t(p.n_split) * size_t(p.part_rows) * size_t(g.D + 1) * 4 : 0;
+  return ST_OK;
+}
+
+// ---------------------------------------------------------------- combine
+// One warp per row: the parts' weights exp(lse_c - M) (M the largest), the
+// weighted rows, and with OWN the row's own keys in the same softmax.  Parts
+// whose LSE is -inf (no key) are not read.  Bound by reading the partials.
+template <typename T, bool OWN>
+__global__ void __launch_bounds__(128) cond_combine(const __grid_constant__ CondParams p) {
+  __shared__ float sq[4][128];
+  st::pdl_trigger();
+  st::pdl_wait();
+  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+  const int D = p.g.D;
+  const long long row = (long long)blockIdx.x * 4 + wp;
+  if (row >= p.part_rows) return;
+  const int r = int(row % p.R);
+  const int w = int(row / p.R % p.HW), unit = int(row / ((long long)p.R * p.HW));
+  const long long off = st::cond_row(p, unit, w, r);
+  const float *part_lse = st::after_wait(p.part_lse), *part_o = st::after_wait(p.part_o);
+  float m = -INFINITY, l = 0.f;                // own keys: running max (log2 units) and sum
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};         // channels lane + 32 i
+  if constexpr (OWN) {
+    const T *q = static_cast<const T *>(st::after_wait(p.q)) + off;
+    const float sl2 = p.scale * 1.4426950408889634f;
+    for (int d = lane; d < D; d += 32) {
+      if constexpr (sizeof(T) == 2) sq[wp][d] = st::bf16_to_f32(q[d]) * sl2;
+      else sq[wp][d] = q[d] * sl2;
+    }
+    __syncwarp();
+    const int b = cond_batch(p, unit) + r / p.G / (p.T0 * p.S0);
+    st::KvSeg sg = p.own;
+    sg.len = st::after_wait(sg.len);
+    sg.offsets = st::after_wait(sg.offsets);
+    const st::KvRange kr = st::kv_range(sg, b);
+    const long long base = (long long)kr.set * (sg.offsets ? 0 : sg.stride_set) + (long long)kr.row0 * sg.stride_l +
+                           (long long)((w * p.G + r % p.G) / (p.G * p.hdiv)) * D;
+    const T *K = static_cast<const T *>(st::after_wait(sg.k)) + base;
+    const T *V = static_cast<const T *>(st::after_wait(sg.v)) + base;
+    const unsigned char *mk = sg.mask ? st::after_wait(sg.mask) + (long long)kr.set * sg.L : nullptr;
+    for (int k0 = 0; k0 < kr.n; k0 += 32) {
+      const int key = k0 + lane;
+      float x = -INFINITY;
+      if (key < kr.n && (!mk || mk[key])) {    // one key per lane
+        const T *kp = K + (long long)key * sg.stride_l;
+        x = 0.f;
+        if constexpr (sizeof(T) == 2) {
+          for (int d = 0; d < D; d += 8) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(kp + d);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x = fmaf(sq[wp][d + 2 * i], __uint_as_float(u[i] << 16), x);
+              x = fmaf(sq[wp][d + 2 * i + 1], __uint_as_float(u[i] & 0xffff0000u), x);
+            }
+          }
+        } else {
+          for (int d = 0; d < D; ++d) x = fmaf(sq[wp][d], kp[d], x);
+        }
+      }
+      float mx = x;
+#pragma unroll
+      for (int y = 16; y > 0; y >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+      const float mn = fmaxf(m, mx);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float corr = exp2f(m - ref), e = exp2f(x - ref);
+      float sum = e;
+#pragma unroll
+      for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+      l = l * corr + sum;
+      m = mn;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] *= corr;
+      const unsigned live = __ballot_sync(0xffffffffu, e != 0.f);
+      const int nk = min(32, kr.n - k0);
+      for (int k = 0; k < nk; ++k) {
+        if (!(live >> k & 1)) continue;        // a key that does not count is not read
+        const float pk = __shfl_sync(0xffffffffu, e, k);
+        const T *vp = V + (long long)(k0 + k) * sg.stride_l;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int d = lane + 32 * i;
+          if (d < D) {
+            if constexpr (sizeof(T) == 2) acc[i] = fmaf(pk, st::bf16_to_f32(vp[d]), acc[i]);
+            else acc[i] = fmaf(pk, vp[d], acc[i]);
+          }
+        }
+      }
+    }
+  }
+  const float L2E = 1.4426950408889634f;
+  const int n = p.n_split;
+  const float l0 = lane < n ? part_lse[(long long)lane * p.part_rows + row] : -INFINITY;
+  const float l1 = lane + 32 < n ? part_lse[(long long)(lane + 32) * p.part_rows + row] : -INFINITY;
+  float M = fmaxf(l0, l1) * L2E;
+#pragma unroll
+  for (int y = 16; y > 0; y >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, y));
+  M = fmaxf(M, m);
+  const float ref = M == -INFINITY ? 0.f : M;
+  const float own = exp2f(m - ref);            // 0 without own keys
+  const float w0 = exp2f(l0 * L2E - ref), w1 = exp2f(l1 * L2E - ref);
+  float sum = w0 + w1;
+#pragma unroll
+  for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+  sum += l * own;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] *= own;
+  for (int c = 0; c < n; ++c) {
+    const float wc = __shfl_sync(0xffffffffu, c < 32 ? w0 : w1, c & 31);
+    if (wc == 0.f) continue;
+    const float *src = part_o + ((long long)c * p.part_rows + row) * D;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (lane + 32 * i < D) acc[i] = fmaf(wc, src[lane + 32 * i], acc[i]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int d = lane + 32 * i;
+    if (d >= D) continue;
+    if (p.o_f32) static_cast<float *>(p.o)[off + d] = acc[i] * inv;
+    else static_cast<uint16_t *>(p.o)[off + d] = st::f32_to_bf16(acc[i] * inv);
+  }
+  if (p.lse && lane == 0) p.lse[st::cond_lse(p, unit, w, r)] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) / L2E;
+}
+
+template <typename T> st_status combine(const CondParams &p, cudaStream_t s) {
+  const long long grid = (p.part_rows + 3) / 4;
+  if (p.own.k) return st::launch_pdl(cond_combine<T, true>, dim3(unsigned(grid)), dim3(128), 0, s, p);
+  return st::launch_pdl(cond_combine<T, false>, dim3(unsigned(grid)), dim3(128), 0, s, p);
+}
+
+st_status run(const st_attn_desc *desc, const st_kv_desc *d0, const st_kv_desc *d1, const void *q, const void *k0,
+              const void *v0, const void *k1, const void *v1, void *o, float *lse, void *ws, size_t ws_bytes,
+              st_stream_t stream) {
+  if (!desc || !d0 || !q || !o) return ST_ERR_NULL;
+  Plan pl;
+  st_status s = make_plan(desc, d0, d1, ws != nullptr, pl);
+  if (s != ST_OK) return s;
+  CondParams &p = pl.p;
+  // pointers of a set without keys may be NULL
+  if ((p.seg[0].L && (!k0 || !v0)) || (d1 && p.seg[1].L && (!k1 || !v1))) return ST_ERR_NULL;
+  if (ws && ws_bytes < pl.workspace) return ST_ERR_SHAPE;
+  const bool bf16 = pl.dtype == ST_BF16;
+  const size_t al = bf16 ? 16 : 4;
+  if (!st::is_aligned(q, al) || !st::is_aligned(o, al) || !st::is_aligned(k0, al) || !st::is_aligned(v0, al) ||
+      !st::is_aligned(k1, al) || !st::is_aligned(v1, al) || !st::is_aligned(lse, 4) || !st::is_aligned(ws, 16))
+    return ST_ERR_ALIGN;
+  for (const KvSeg &sg : p.seg)
+    if (!st::is_aligned(sg.len, 4) || !st::is_aligned(sg.offsets, 4)) return ST_ERR_ALIGN;
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.seg[0].k = k0;
+  p.seg[0].v = v0;
+  p.seg[1].k = k1;
+  p.seg[1].v = v1;
+  const bool own = d1 && p.n_seg == 1;
+  p.own = own ? p.seg[1] : KvSeg{};
+  if (own && !p.own.L) p.own.k = p.own.v = q;  // no keys: never read
+  if (pl.workspace) {
+    p.part_o = static_cast<float *>(ws);
+    p.part_lse = p.part_o + (long long)p.n_split * p.part_rows * p.g.D;
+  }
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  s = st::cond_simt(p, pl.dtype, st);
+  if (s != ST_OK || !pl.workspace) return s;
+  return bf16 ? combine<uint16_t>(p, st) : combine<float>(p, st);
+}
+
+size_t ws_bytes(const st_attn_desc *desc, const st_kv_desc *d0, const st_kv_desc *d1) {
+  Plan pl;
+  if (!desc || !d0 || make_plan(desc, d0, d1, true, pl) != ST_OK) return 0;
+  return pl.workspace;
+}
+
+}  // namespace
+
+ST_API st_status st_attn_cross(const st_attn_desc *desc, const st_kv_desc *kv, const void *q, const void *k,
+                               const void *v, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                               st_stream_t stream) {
+  return run(desc, kv, nullptr, q, k, v, nullptr, nullptr, o, lse, workspace, workspace_bytes, stream);
+}
+
+ST_API size_t st_attn_cross_workspace_bytes(const st_attn_desc *desc, const st_kv_desc *kv) {
+  return ws_bytes(desc, kv, nullptr);
+}
+
+ST_API st_status st_attn_prefix(const st_attn_desc *desc, const st_kv_desc *prefix, const st_kv_desc *own,
+                                const void *q, const void *k_prefix, const void *v_prefix, const void *k,
+                                const void *v, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                st_stream_t stream) {
+  if (!own) return ST_ERR_NULL;
+  return run(desc, prefix, own, q, k_prefix, v_prefix, k, v, o, lse, workspace, workspace_bytes, stream);
+}
+
+ST_API size_t st_attn_prefix_workspace_bytes(const st_attn_desc *desc, const st_kv_desc *prefix,
+                                             const st_kv_desc *own) {
+  return own ? ws_bytes(desc, prefix, own) : 0;
+}

@@ -1,0 +1,246 @@
+// Conditioning attention on the fp32 FMA pipes.
+//
+// fp32 workloads ask for 1e-4 or better, which rules out single tf32 or bf16
+// products.  A CTA of 256 threads owns 64 query rows of one (unit, head): Q
+// stays in shared memory, keys come in tiles of 64, thread (ty, tx) holds a
+// 4 x 4 piece of the scores (rows 4 ty .. 4 ty + 3, keys tx + 16 j) and 4
+// rows x 4 columns per 64 channels of the output.  The softmax is the online
+// form (running max and sum per row in fp32); the probabilities replace the K
+// tile in shared memory, so two CTAs fit an SM at head dim 128 and one loads
+// while the other multiplies.
+#include <math.h>
+
+#include "cond.cuh"
+
+namespace {
+
+constexpr int BM = 64, BN = 64, NT = 256;
+
+template <typename T> __device__ __forceinline__ float4 load4(const T *p);
+template <> __device__ __forceinline__ float4 load4<float>(const float *p) {
+  return make_float4(p[0], p[1], p[2], p[3]);
+}
+template <> __device__ __forceinline__ float4 load4<uint16_t>(const uint16_t *p) {
+  return make_float4(st::bf16_to_f32(p[0]), st::bf16_to_f32(p[1]), st::bf16_to_f32(p[2]), st::bf16_to_f32(p[3]));
+}
+
+// NC: 64-channel chunks of the head (D <= 64 * NC)
+template <typename T, int NC>
+__global__ void __launch_bounds__(NT) cond_simt_kernel(const __grid_constant__ st::CondParams p, int row_blocks) {
+  extern __shared__ float sm[];
+  const int D = p.g.D, DP = (D + 3) / 4 * 4, PQ = DP + 4;
+  float *sQ = sm, *sK = sQ + BM * PQ, *sV = sK + (BM * (PQ > BN + 4 ? PQ : BN + 4));
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  long long x = blockIdx.x;
+  const int rb = int(x % row_blocks);
+  x /= row_blocks;
+  const int sp = int(x % p.n_split);
+  x /= p.n_split;
+  const int w = int(x % p.HW), unit = int(x / p.HW);
+  const int rows = p.R, r0 = rb * BM;
+  const int kvh = w / p.hdiv;
+  const T *Q = static_cast<const T *>(p.q);
+  for (int i = tid; i < BM * (DP / 4); i += NT) {
+    const int r = i / (DP / 4), c = (i - r * (DP / 4)) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r0 + r < rows) {
+      const T *src = Q + st::cond_row(p, unit, w, r0 + r) + c;
+      if (c + 4 <= D) v = load4(src);
+      else {
+        float *e = &v.x;
+        for (int d = 0; c + d < D; ++d) {
+          if constexpr (sizeof(T) == 2) e[d] = st::bf16_to_f32(src[d]);
+          else e[d] = src[d];
+        }
+      }
+    }
+    *reinterpret_cast<float4 *>(sQ + r * PQ + c) = v;
+  }
+  float m[4], l[4], acc[4][NC][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][c][e] = 0.f;
+  }
+  const float sl2 = p.scale * 1.4426950408889634f;
+  st::KvRange kr[2];
+  int steps[2] = {0, 0};
+  for (int g = 0; g < p.n_seg; ++g) {
+    kr[g] = st::kv_range(p.seg[g], st::cond_batch(p, unit));
+    steps[g] = (kr[g].n + BN - 1) / BN;
+  }
+  const long long total = (long long)steps[0] + steps[1];
+  const int j0 = int(total * sp / p.n_split), j1 = int(total * (sp + 1) / p.n_split);
+  for (int j = j0; j < j1; ++j) {
+    const int g = j < steps[0] ? 0 : 1;
+    const int key0 = (g ? j - steps[0] : j) * BN;
+    const st::KvSeg &sg = p.seg[g];
+    const int nv = min(BN, kr[g].n - key0);
+    const long long base = (long long)kr[g].set * (sg.offsets ? 0 : sg.stride_set) +
+                           (long long)(kr[g].row0 + key0) * sg.stride_l + (long long)kvh * D;
+    const T *Kp = static_cast<const T *>(sg.k) + base, *Vp = static_cast<const T *>(sg.v) + base;
+    const unsigned char *mk = sg.mask ? sg.mask + (long long)kr[g].set * sg.L + key0 : nullptr;
+    __syncthreads();
+    for (int i = tid; i < BN * (DP / 4); i += NT) {
+      const int r = i / (DP / 4), c = (i - r * (DP / 4)) * 4;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+      // a key that does not count is never read, so its V cannot reach the sum
+      if (r < nv && (!mk || mk[r])) {
+        const long long off = (long long)r * sg.stride_l + c;
+        if (c + 4 <= D) {
+          a = load4(Kp + off);
+          b = load4(Vp + off);
+        } else {
+          float *ea = &a.x, *eb = &b.x;
+          for (int d = 0; c + d < D; ++d) {
+            if constexpr (sizeof(T) == 2) {
+              ea[d] = st::bf16_to_f32(Kp[off + d]);
+              eb[d] = st::bf16_to_f32(Vp[off + d]);
+            } else {
+              ea[d] = Kp[off + d];
+              eb[d] = Vp[off + d];
+            }
+          }
+        }
+      }
+      *reinterpret_cast<float4 *>(sK + r * PQ + c) = a;
+      *reinterpret_cast<float4 *>(sV + r * DP + c) = b;
+    }
+    __syncthreads();
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+    for (int d = 0; d < DP; d += 4) {
+      float4 a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(sQ + (4 * ty + i) * PQ + d);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * e) * PQ + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[i][e] = fmaf(a[i].x, b[e].x, s[i][e]);
+          s[i][e] = fmaf(a[i].y, b[e].y, s[i][e]);
+          s[i][e] = fmaf(a[i].z, b[e].z, s[i][e]);
+          s[i][e] = fmaf(a[i].w, b[e].w, s[i][e]);
+        }
+    }
+    bool keep[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = tx + 16 * e;
+      keep[e] = c < nv && (!mk || mk[c]);
+    }
+    __syncthreads();                           // every thread has read the K tile
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[i][e] = keep[e] ? s[i][e] * sl2 : -INFINITY;
+        mx = fmaxf(mx, s[i][e]);
+      }
+#pragma unroll
+      for (int y = 8; y > 0; y >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+      const float mn = fmaxf(m[i], mx);
+      const float ref = mn == -INFINITY ? 0.f : mn;   // nothing counted yet: every weight is 0
+      const float corr = exp2f(m[i] - ref);
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[i][e] = exp2f(s[i][e] - ref);
+        sum += s[i][e];
+        sK[(4 * ty + i) * (BN + 4) + tx + 16 * e] = s[i][e];
+      }
+#pragma unroll
+      for (int y = 8; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+      l[i] = l[i] * corr + sum;
+      m[i] = mn;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][c][e] *= corr;
+    }
+    __syncthreads();
+    for (int k = 0; k < BN; k += 4) {
+      float4 pr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pr[i] = *reinterpret_cast<const float4 *>(sK + (4 * ty + i) * (BN + 4) + k);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int col = c * 64 + tx * 4;
+          if (col < DP) {
+            const float4 v = *reinterpret_cast<const float4 *>(sV + (k + kk) * DP + col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float pv = kk == 0 ? pr[i].x : kk == 1 ? pr[i].y : kk == 2 ? pr[i].z : pr[i].w;
+              acc[i][c][0] = fmaf(pv, v.x, acc[i][c][0]);
+              acc[i][c][1] = fmaf(pv, v.y, acc[i][c][1]);
+              acc[i][c][2] = fmaf(pv, v.z, acc[i][c][2]);
+              acc[i][c][3] = fmaf(pv, v.w, acc[i][c][3]);
+            }
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 4 * ty + i;
+    if (r >= rows) continue;
+    const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);   // NaN scores stay NaN
+    const float lse = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+    const long long prow = (long long)sp * p.part_rows + ((long long)unit * p.HW + w) * rows + r;
+    const long long off = p.part_o ? prow * D : st::cond_row(p, unit, w, r);
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d = c * 64 + tx * 4 + e;
+        if (d >= D) continue;
+        const float y = acc[i][c][e] * inv;
+        if (p.part_o) p.part_o[off + d] = y;
+        else if (sizeof(T) == 4 || p.o_f32) static_cast<float *>(p.o)[off + d] = y;
+        else static_cast<uint16_t *>(p.o)[off + d] = st::f32_to_bf16(y);
+      }
+    if (tx == 0) {
+      if (p.part_o) p.part_lse[prow] = lse;
+      else if (p.lse) p.lse[st::cond_lse(p, unit, w, r)] = lse;
+    }
+  }
+}
+
+template <typename T, int NC> st_status launch(const st::CondParams &p, cudaStream_t s) {
+  const int DP = (p.g.D + 3) / 4 * 4, PQ = DP + 4;
+  const size_t smem = size_t(BM * PQ + BM * (PQ > BN + 4 ? PQ : BN + 4) + BN * DP) * 4;
+  const int row_blocks = (p.R + BM - 1) / BM;
+  const long long grid = (long long)row_blocks * p.n_split * p.HW * st::cond_units(p);
+  if (grid > 0x7fffffffLL) return ST_ERR_SHAPE;
+  auto kern = cond_simt_kernel<T, NC>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+    return ST_ERR_CUDA;
+  kern<<<unsigned(grid), NT, smem, s>>>(p, row_blocks);
+  return st::launch_status();
+}
+
+}  // namespace
+
+namespace st {
+
+st_status cond_simt(const CondParams &p, st_dtype dtype, cudaStream_t s) {
+  if (p.g.D > 128) return ST_ERR_UNSUPPORTED;
+  if (dtype == ST_F32) return p.g.D <= 64 ? launch<float, 1>(p, s) : launch<float, 2>(p, s);
+  return p.g.D <= 64 ? launch<uint16_t, 1>(p, s) : launch<uint16_t, 2>(p, s);
+}
+
+}  // namespace st
+namespace st { CondTile cond_tile(int) { return CondTile{64, 64}; } }

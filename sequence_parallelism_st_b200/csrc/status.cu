@@ -1,14 +1,14 @@
 // Status strings, device-status check and per-device SM count.
 #include <mutex>
 
-#include "common.cuh"
+#include "cond.cuh"
 
 namespace st {
 
 // SM budget of the launches this host thread issues (0: the whole device).
 thread_local int t_sm_budget = 0;
 
-int num_sms() {
+int device_sms() {
   static int cache[64] = {0};
   int dev = 0;
   int n = 148;
@@ -20,6 +20,11 @@ int num_sms() {
     }
     n = cache[dev];
   }
+  return n;
+}
+
+int num_sms() {
+  const int n = device_sms();
   return t_sm_budget > 0 && t_sm_budget < n ? t_sm_budget : n;
 }
 
