@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libstattn.so")
 
 SOURCES = ["status.cu", "relayout.cu", "vmajor.cu", "merge.cu", "attn_api.cu",
            "attn_simt.cu", "attn_temporal.cu", "attn_spatial_sm100.cu", "qk_norm_rope.cu",
-           "cond_api.cu", "cond_simt.cu"]
+           "cond_api.cu", "cond_simt.cu", "cond_sm100.cu"]
 HEADERS = ["common.cuh", "attn_geom.cuh", "cond.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -243,4 +243,3 @@ st_status cond_simt(const CondParams &p, st_dtype dtype, cudaStream_t s) {
 }
 
 }  // namespace st
-namespace st { CondTile cond_tile(int) { return CondTile{64, 64}; } }
