@@ -77,23 +77,24 @@ template <int D> struct Cfg {
   static constexpr bool ONES = DPV > D;
   static constexpr int TW = BN + DPV;                  // TMEM columns of a tile: S (P over it), O
   static_assert(NT * TW <= 512, "TMEM");
-  static constexpr int NQ = D <= 64 ? 6 : (D <= 80 ? 5 : (D <= 96 ? 4 : 2));   // Q tiles
-  // per epilogue warp: 32 rows of O, a 128-byte chunk at a time for head dim 128
+  // Q tiles: QB slots per row tile, its own so that its issuer sees every phase
+  static constexpr int QB = D == 32 ? 2 : 1, NQ = NT * QB;
+  // staging of a warp's 32 rows of O, a 128-byte chunk at a time for head dim 128
   static constexpr int STG = 32 * (D == 128 ? SW0 : SW0 + SW1);
-  static constexpr int STAT = NT * 2 * BLOCK_M * 4;
-  static constexpr int TAIL = 4 * STG + STAT + 2 * SET_TABLE * 8 + 1024;       // + barriers
+  static constexpr int NSTG = NT;                      // one per tile
+  static constexpr int TAIL = 4 * NSTG * STG + 2 * SET_TABLE * 8 + 512 + (NT == 3 ? 1024 : 512);   // + items, barriers
   static constexpr int NS_RAW = (232448 - 1024 - TAIL - NQ * QTILE) / (KTILE + VTILE);
   static constexpr int NS = NS_RAW > 8 ? 8 : NS_RAW;   // K/V stages
   static constexpr int SMEM = 1024 + NQ * QTILE + NS * (KTILE + VTILE) + TAIL;
   static_assert(SMEM <= 232448 && NS >= 2, "shared memory");
-  // warps: softmax of the tiles, epilogue, then loader, issuers, V helper
-  static constexpr int W_EPI = 4 * NT, W_LOAD = W_EPI + 4, W_MMA = W_LOAD + 1, W_FIX = W_MMA + NT;
-  static constexpr int MISC = NT == 3 ? 8 : 4;
-  static constexpr int THREADS = 32 * (W_LOAD + MISC);
+  // warps: softmax and epilogue of the tiles (4 each), then loader, issuers, V
+  // helper, scheduler; the rest of the last two warpgroups idles
+  static constexpr int W_LOAD = 4 * NT, W_MMA = W_LOAD + 1, W_FIX = W_MMA + NT, W_SCHED = W_FIX + 1;
+  static constexpr int THREADS = 32 * (W_LOAD + 8);
   // registers: granted at launch, then moved to the softmax (setmaxnreg)
-  static constexpr int R_LAUNCH = NT == 3 ? 80 : 128;
-  static constexpr int R_SOFT = NT == 3 ? 104 : 184, R_EPI = NT == 3 ? 80 : 88, R_MISC = NT == 3 ? 40 : 48;
-  static_assert(128 * NT * R_SOFT + 128 * R_EPI + 32 * MISC * R_MISC <= THREADS * R_LAUNCH, "register split");
+  static constexpr int R_LAUNCH = NT == 3 ? 96 : 128;
+  static constexpr int R_SOFT = NT == 3 ? 120 : 200, R_MISC = 56;
+  static_assert(128 * NT * R_SOFT + 256 * R_MISC <= THREADS * R_LAUNCH, "register split");
 };
 
 // ---------------------------------------------------------------- exp2
@@ -187,14 +188,11 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity, ui
       : "memory");
   return ok != 0;
 }
-// Bounded wait for a phase: SPIN polls (a polling thread resumes sooner than a
-// suspended one; used on the MMA chain), then sleeps in the barrier; the
-// clock and the abort epoch are only consulted after a sleep of ~0.1 ms that
-// ended without the phase.
-template <int SPIN = 0>
+// Bounded wait for a phase by one thread: it sleeps in the barrier; the clock
+// and the abort epoch are only consulted after a sleep of ~0.1 ms that ended
+// without the phase.
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint32_t epoch, int site) {
-  for (int i = 0; i <= SPIN; ++i)
-    if (mbar_test(bar, parity)) return true;
+  if (mbar_test(bar, parity)) return true;
   const unsigned long long t0 = globaltimer();
   while (true) {
     if (mbar_try_wait(bar, parity, 100000u)) return true;
@@ -204,6 +202,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint32
       atomicExch(&g_cond_abort_epoch, epoch);
       return false;
     }
+  }
+}
+// The same by a whole warp, whose lanes agree on the answer (a warp that
+// gives up does so in all lanes).  SPIN polls come first: a polling warp
+// resumes sooner than a suspended one, which the MMA chain notices.
+template <int SPIN = 0>
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t epoch, int site) {
+  for (int i = 0; i <= SPIN; ++i)
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  const unsigned long long t0 = globaltimer();
+  while (true) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity, 100000u))) return true;
+    bool stop = *reinterpret_cast<volatile unsigned int *>(&g_cond_abort_epoch) == epoch;
+    if (globaltimer() - t0 > WAIT_NS) {
+      atomicOr(&g_cond_error, 1u << (site & 31));
+      atomicExch(&g_cond_abort_epoch, epoch);
+      stop = true;
+    }
+    if (__any_sync(0xffffffffu, stop)) return false;
   }
 }
 // The same for the end of work already issued, whatever the abort epoch.
@@ -299,6 +316,18 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
+// Lane 0's value, known to the compiler to be the same in the whole warp.
+template <typename T> __device__ __forceinline__ T uniform(T v) { return T(__shfl_sync(0xffffffffu, v, 0)); }
+// True in one lane of the converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok));
+  return ok != 0;
+}
 // 16-byte chunk f of row r of a swizzled tile with rows of `bytes`.
 template <int BYTES> __device__ __forceinline__ int swz(int r, int f) {
   return f ^ (BYTES == 128 ? (r & 7) : (BYTES == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1)));
@@ -323,12 +352,24 @@ struct Args {
   uint32_t epoch;
 };
 
-struct Item {
-  int r0, n_qt, w, unit, kvh, split;
-  int set0, row0, n0, set1, row1, n1;   // the segments' sets, first rows and keys
-  int s0;                      // steps of segment 0
-  int j0, n_kv;                // first step and steps of this item
+// One item, written by the scheduler warp and read by every other.
+struct alignas(16) Item {
+  int n_qt;                    // row tiles; 0: no more items
+  int n_kv;                    // steps of this item
+  int n0, n1;                  // keys of the segments
+  int s0, j0;                  // steps of segment 0; first step
+  int set0, set1;              // the segments' sets
+  int row0, row1;              // first rows of their key ranges (packed)
+  int r0, w, unit, split;      // first row, walked head, unit, part of the keys
+  int c3, c4;                  // the unit's frame coordinates in the Q and O maps
+  int kvh;
+  int fresh;                   // its keys are not those of the item before
+  int release;                 // nor those of the item after
+  int qb;                      // row block of the unit
+  int pad[4];
 };
+constexpr int ITEMS = 4;       // items in flight between the scheduler and the others
+static_assert(ITEMS * sizeof(Item) <= 512, "item ring");
 
 struct Step {
   int seg, key, valid;         // segment, first key in its range, keys that exist
@@ -346,22 +387,34 @@ template <int BN> __device__ __forceinline__ Step step_of(const Item &it, int j)
   return s;
 }
 
+template <int D> __device__ __forceinline__ void rows_of(const Args &a, Item &it) {
+  it.r0 = it.qb * Cfg<D>::NT * a.tile_rows;
+  const int left = a.c.R - it.r0;
+  it.n_qt = left > 2 * a.tile_rows && Cfg<D>::NT > 2 ? 3 : (left > a.tile_rows ? 2 : 1);
+}
+
 // q block fastest, then split, head, unit.  table: the segments' key ranges (row, n).
 template <int D>
 __device__ __forceinline__ Item decode(const Args &a, const int2 *table, int x) {
   using K = Cfg<D>;
   Item it;
   const uint32_t y = st::fdiv(uint32_t(x), a.dqb);
-  const int qb = x - int(y) * a.q_blocks;
+  it.qb = x - int(y) * a.q_blocks;
   const uint32_t z = st::fdiv(y, a.dsplit);
   it.split = int(y) - int(z) * a.c.n_split;
   it.unit = int(st::fdiv(z, a.dhw));
   it.w = int(z) - it.unit * a.c.HW;
   it.kvh = int(st::fdiv(uint32_t(it.w), a.dkv));
-  it.r0 = qb * K::NT * a.tile_rows;
-  const int left = a.c.R - it.r0;
-  it.n_qt = left > 2 * a.tile_rows && K::NT > 2 ? 3 : (left > a.tile_rows ? 2 : 1);
-  const int b = int(st::fdiv(uint32_t(it.unit), a.dt)) * a.c.bm;
+  rows_of<D>(a, it);
+  const int ub = int(st::fdiv(uint32_t(it.unit), a.dt)), t = it.unit - ub * a.c.g.T;
+  if (a.c.g.tblk != a.c.g.T) {
+    it.c3 = t % a.c.g.tblk;
+    it.c4 = ub * (a.c.g.T / a.c.g.tblk) + t / a.c.g.tblk;
+  } else {
+    it.c3 = t;
+    it.c4 = ub;
+  }
+  const int b = ub * a.c.bm;
   auto range = [&](int g, int &set, int &row, int &n) {
     set = row = n = 0;
     if (g >= a.c.n_seg) return;
@@ -395,8 +448,9 @@ __device__ __forceinline__ bool same_keys(const Item &a, const Item &b) {
 }
 
 // The items of a CTA: consecutive ones when K and V stay resident, else every
-// gridDim-th, so that the CTAs that run together share K/V tiles in L2.
-struct Walk {
+// gridDim-th, so that the CTAs that run together share K/V tiles in L2.  The
+// next row block of the same keys needs no division.
+template <int D> struct Walk {
   int x, end, inc;
   __device__ __forceinline__ explicit Walk(const Args &a) {
     if (a.resident) {
@@ -408,6 +462,35 @@ struct Walk {
       end = a.n_items;
       inc = gridDim.x;
     }
+  }
+  __device__ __forceinline__ Item after(const Args &a, const int2 *table, const Item &it) const {
+    Item nx = it;
+    if (x + inc >= end) {
+      nx.n_qt = 0;
+    } else if (inc == 1 && it.qb + 1 < a.q_blocks) {
+      ++nx.qb;
+      rows_of<D>(a, nx);
+    } else {
+      nx = decode<D>(a, table, x + inc);
+    }
+    nx.fresh = !same_keys(it, nx);
+    return nx;
+  }
+};
+
+// A reader's place in the ring of items.
+struct Reader {
+  uint32_t i = 0;
+  // The next item, once it is there: the caller reads what it needs, then the
+  // warp hands it back.
+  template <int SPIN>
+  __device__ __forceinline__ const Item *get(const Item *items, uint64_t *full, uint32_t epoch, int site) const {
+    return warp_wait<SPIN>(full + i % ITEMS, (i / ITEMS) & 1, epoch, site) ? items + i % ITEMS : nullptr;
+  }
+  __device__ __forceinline__ void done(uint64_t *empty, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty + i % ITEMS);
+    ++i;
   }
 };
 
@@ -425,24 +508,23 @@ template <int D>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     cond_attn_sm100(const __grid_constant__ Maps mp, const __grid_constant__ Args a) {
   using K = Cfg<D>;
-  constexpr int NT = K::NT, NS = K::NS, NQ = K::NQ, BN = K::BN;
+  constexpr int NT = K::NT, NS = K::NS, NQ = K::NQ, QB = K::QB, BN = K::BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sQ = base;
   uint8_t *sK = sQ + NQ * K::QTILE;
   uint8_t *sV = sK + NS * K::KTILE;
   uint8_t *sStg = sV + NS * K::VTILE;
-  float *sStat = reinterpret_cast<float *>(sStg + 4 * K::STG);   // [tile][m | l][row]
-  int2 *sSet = reinterpret_cast<int2 *>(sStg + 4 * K::STG + K::STAT);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sSet + 2 * SET_TABLE);
+  int2 *sSet = reinterpret_cast<int2 *>(sStg + 4 * K::NSTG * K::STG);
+  Item *sItem = reinterpret_cast<Item *>(sSet + 2 * SET_TABLE);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sItem + ITEMS);
   uint64_t *q_full = bars, *q_empty = q_full + NQ;
   uint64_t *k_full = q_empty + NQ, *k_empty = k_full + NS;       // k_empty, v_empty: one arrival per tile
   uint64_t *v_full = k_empty + NS, *v_empty = v_full + NS, *v_ready = v_empty + NS;
   uint64_t *s_full = v_ready + NS, *p_full = s_full + NT;
-  uint64_t *o_full = p_full + NT, *o_empty = o_full + NT;
-  uint64_t *stat_full = o_empty + NT, *stat_empty = stat_full + NT;
-  uint64_t *mma_done = stat_empty + NT;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + NT);
+  uint64_t *o_full = p_full + NT, *mma_done = o_full + NT;
+  uint64_t *item_full = mma_done + NT, *item_empty = item_full + ITEMS;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(item_empty + ITEMS);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -461,10 +543,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, BLOCK_M);
       mbar_init(o_full + i, 1);
-      mbar_init(o_empty + i, BLOCK_M);
-      mbar_init(stat_full + i, BLOCK_M);
-      mbar_init(stat_empty + i, BLOCK_M);
       mbar_init(mma_done + i, 1);
+    }
+    for (int i = 0; i < ITEMS; ++i) {
+      mbar_init(item_full + i, 1);
+      mbar_init(item_empty + i, 5 * NT + 2);   // softmax warps, issuers, loader, helper
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -497,32 +580,27 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   if (warp >= K::W_LOAD) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K::R_MISC));
     if (warp == K::W_LOAD) {
-      if (lane == 0) {
-        // ================= TMA producer =================
-        bool ok = true;
-        Ring<NS> ring;
-        uint32_t qc = 0;                              // Q tiles so far
-        int last_kv = -1;                             // streaming: ring position of the last K/V issued
-        int loaded = 0;                               // resident: stages loaded in this run
-        Walk wk(a);
-        Item prev;
-        bool first = true;
-        for (int x = wk.x; x < wk.end && ok; x += wk.inc) {
-          const Item it = decode<D>(a, sSet, x);
-          const bool load_kv = !resident || first || !same_keys(prev, it);
+      // ================= TMA producer =================
+      bool ok = true;
+      Ring<NS> ring;
+      Reader rd;
+      uint32_t qc[NT];                                // Q tiles so far
+#pragma unroll
+      for (int X = 0; X < NT; ++X) qc[X] = 0;
+      int last_kv = -1;                               // streaming: ring position of the last K/V issued
+      int loaded = 0;                                 // resident: stages loaded in this run
+      bool first = true;
+      while (ok) {
+        const Item *ip = rd.get<0>(sItem, item_full, epoch, 15);
+        if (!(ok = ip != nullptr)) break;
+        const Item it = *ip;
+        rd.done(item_empty, lane);
+        if (it.n_qt == 0) break;
+        if (lane == 0) {
+          const bool load_kv = !resident || it.fresh;
           if (resident && load_kv && !first) ++ring.run;
-          const int n = resident ? (load_kv ? a.max_steps : 1) : (it.n_kv > 0 ? it.n_kv : 0);
-          int c3 = it.unit, c4 = 0;
-          {
-            const int b = int(st::fdiv(uint32_t(it.unit), a.dt)), t = it.unit - b * a.c.g.T;
-            if (a.c.g.tblk != a.c.g.T) {
-              c3 = t % a.c.g.tblk;
-              c4 = b * (a.c.g.T / a.c.g.tblk) + t / a.c.g.tblk;
-            } else {
-              c3 = t;
-              c4 = b;
-            }
-          }
+          first = false;
+          const int n = resident ? (load_kv ? a.max_steps : 1) : it.n_kv;
           for (int j = 0; j < n && ok; ++j) {
             const int st = ring.stage(resident, j);
             const uint32_t ph = ring.phase(resident, j);
@@ -544,9 +622,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
               }
             }
             if (j == 0 && it.n_kv > 0) {
-              for (int X = 0; X < it.n_qt && ok; ++X, ++qc) {
-                const int qs = qc % NQ;
-                if (!(ok = mbar_wait(q_empty + qs, ((qc / NQ) & 1) ^ 1, epoch, 0))) break;
+#pragma unroll
+              for (int X = 0; X < NT; ++X) {
+                if (X >= it.n_qt || !ok) continue;
+                const int qs = X * QB + qc[X] % QB;
+                if (!(ok = mbar_wait(q_empty + qs, ((qc[X] / QB) & 1) ^ 1, epoch, 0))) continue;
+                ++qc[X];
                 uint8_t *dst = sQ + qs * K::QTILE;
                 const int row = it.r0 + X * a.tile_rows;
                 mbar_expect_tx(q_full + qs, a.tile_rows * (K::SW0 + K::SW1));
@@ -554,8 +635,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                   tma_load_5d(dst, &mp.q0, q_full + qs, 0, 0, it.w, row / a.c.G, it.unit);
                   if (K::C1) tma_load_5d(dst + K::QT0, &mp.q1, q_full + qs, 64, 0, it.w, row / a.c.G, it.unit);
                 } else {
-                  tma_load_5d(dst, &mp.q0, q_full + qs, 0, it.w, row, c3, c4);
-                  if (K::C1) tma_load_5d(dst + K::QT0, &mp.q1, q_full + qs, 64, it.w, row, c3, c4);
+                  tma_load_5d(dst, &mp.q0, q_full + qs, 0, it.w, row, it.c3, it.c4);
+                  if (K::C1) tma_load_5d(dst + K::QT0, &mp.q1, q_full + qs, 64, it.w, row, it.c3, it.c4);
                 }
               }
               if (!ok) break;
@@ -574,106 +655,182 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             }
           }
           if (!resident) ring.pos += it.n_kv;
-          prev = it;
-          first = false;
         }
-        if (!ok) {
-          // the last load issued into every stage and Q slot (a wait for one
-          // that was not issued runs into its limit)
-          if (resident) {
-            for (int j = 0; j < loaded; ++j) {
-              mbar_drain(k_full + j, ring.run & 1);
-              mbar_drain(v_full + j, ring.run & 1);
-            }
-          } else {
-            for (int i = (last_kv - NS + 1 > 0 ? last_kv - NS + 1 : 0); i <= last_kv; ++i) {
-              mbar_drain(k_full + i % NS, (i / NS) & 1);
-              mbar_drain(v_full + i % NS, (i / NS) & 1);
-            }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      }
+      if (!ok && lane == 0) {
+        // the last load issued into every stage and Q slot (a wait for one
+        // that was not issued runs into its limit)
+        if (resident) {
+          for (int j = 0; j < loaded; ++j) {
+            mbar_drain(k_full + j, ring.run & 1);
+            mbar_drain(v_full + j, ring.run & 1);
           }
-          for (int i = (int(qc) - NQ > 0 ? int(qc) - NQ : 0); i < int(qc); ++i) mbar_drain(q_full + i % NQ, (i / NQ) & 1);
+        } else {
+          for (int i = (last_kv - NS + 1 > 0 ? last_kv - NS + 1 : 0); i <= last_kv; ++i) {
+            mbar_drain(k_full + i % NS, (i / NS) & 1);
+            mbar_drain(v_full + i % NS, (i / NS) & 1);
+          }
         }
+#pragma unroll
+        for (int X = 0; X < NT; ++X)
+          for (int i = (int(qc[X]) > QB ? int(qc[X]) - QB : 0); i < int(qc[X]); ++i)
+            mbar_drain(q_full + X * QB + i % QB, (i / QB) & 1);
       }
       __syncwarp();
     } else if (warp >= K::W_MMA && warp < K::W_MMA + NT) {
-      if (lane == 0) {
-        // ================= issuer of tile X =================
-        const int X = warp - K::W_MMA;
-        constexpr uint32_t IDS = idesc_bf16(BLOCK_M, BN, 0, 0), IDPV = idesc_bf16(BLOCK_M, K::DPV, 0, 1);
-        const uint32_t aK = smem_u32(sK), aV = smem_u32(sV);
-        const uint32_t dS = tmem + X * K::TW, dO = dS + BN;
-        bool ok = true;
-        Ring<NS> ring;
-        uint32_t qc = 0, steps = 0, oc = 0;            // Q tiles of the CTA; steps and items of this tile
-        Walk wk(a);
-        Item it;
-        if (wk.x < wk.end) it = decode<D>(a, sSet, wk.x);
-        for (int x = wk.x; x < wk.end && ok; x += wk.inc) {
-          // resident: the stages are handed back at the last item of a run
-          Item nx = it;
-          const bool more = x + wk.inc < wk.end;
-          if (more) nx = decode<D>(a, sSet, x + wk.inc);
-          const bool release = !resident || !more || !same_keys(it, nx);
-          if (X < it.n_qt && it.n_kv > 0) {
-            const uint32_t qi = qc + X;
-            if (!(ok = mbar_wait(q_full + qi % NQ, (qi / NQ) & 1, epoch, 3))) break;
-            const uint32_t qa = smem_u32(sQ) + (qi % NQ) * K::QTILE;
-            for (int j = 0; j < it.n_kv; ++j, ++steps) {
-              const int st = ring.stage(resident, j);
-              const uint32_t ph = ring.phase(resident, j);
-              if (!(ok = mbar_wait<32>(k_full + st, ph, epoch, 4))) break;
-              tc_fence_after();
-              const uint32_t ka = aK + st * K::KTILE;
+      // ================= issuer of tile X =================
+      // P of a step ready -> its PV, then S of the next step (of the next item
+      // after the last) into the same columns.  The whole warp walks the loop
+      // and one elected lane issues, so addresses and descriptors stay in
+      // uniform registers: computed by one diverged lane, an MMA took about 200
+      // cycles to issue.
+      const int X = uniform(warp) - K::W_MMA;
+      constexpr uint32_t IDS = idesc_bf16(BLOCK_M, BN, 0, 0), IDPV = idesc_bf16(BLOCK_M, K::DPV, 0, 1);
+      const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
+      const uint32_t dS = uniform(tmem) + X * K::TW, dO = dS + BN;
+      const bool leader = elect_one();
+      bool ok = true;
+      Ring<NS> ring;
+      Reader rd;
+      uint32_t qc = 0, steps = 0;                      // items and steps of this tile
+      auto issue_s = [&](uint32_t qs, int st) {        // Q in slot qs, K in stage st
+        const uint32_t qa = aQ + qs * K::QTILE, ka = aK + st * K::KTILE;
 #pragma unroll
-              for (int kk = 0; kk < K::C0 / 16; ++kk)
-                mma_ss(dS, sdesc<16, 8 * K::SW0, layout_of(K::SW0)>(qa + kk * 32),
-                       sdesc<16, 8 * K::SW0, layout_of(K::SW0)>(ka + kk * 32), IDS, kk > 0);
-              if (K::C1) {
+        for (int kk = 0; kk < K::C0 / 16; ++kk)
+          mma_ss(dS, sdesc<16, 8 * K::SW0, layout_of(K::SW0)>(qa + kk * 32),
+                 sdesc<16, 8 * K::SW0, layout_of(K::SW0)>(ka + kk * 32), IDS, kk > 0);
+        if (K::C1) {
 #pragma unroll
-                for (int kk = 0; kk < K::C1X / 16; ++kk)
-                  mma_ss(dS, sdesc<16, 8 * K::SW1X, layout_of(K::SW1X)>(qa + K::QT0 + kk * 32),
-                         sdesc<16, 8 * K::SW1X, layout_of(K::SW1X)>(ka + K::KT0 + kk * 32), IDS, 1);
-              }
-              tc_commit(s_full + X);
-              if (release) tc_commit(k_empty + st);
-              if (j + 1 == it.n_kv) tc_commit(q_empty + qi % NQ);
-              if (!(ok = mbar_wait<32>(v_ready + st, ph, epoch, 5))) break;
-              // O of the tile's previous item read out by the epilogue
-              if (j == 0 && !(ok = mbar_wait<32>(o_empty + X, (oc & 1) ^ 1, epoch, 6))) break;
-              if (!(ok = mbar_wait<32>(p_full + X, steps & 1, epoch, 7))) break;
-              tc_fence_after();
+          for (int kk = 0; kk < K::C1X / 16; ++kk)
+            mma_ss(dS, sdesc<16, 8 * K::SW1X, layout_of(K::SW1X)>(qa + K::QT0 + kk * 32),
+                   sdesc<16, 8 * K::SW1X, layout_of(K::SW1X)>(ka + K::KT0 + kk * 32), IDS, 1);
+        }
+        tc_commit(s_full + X);
+      };
+      int n = 0, n_qt = 0;
+      bool fresh = false, release = false;
+      auto fetch = [&]() -> bool {                     // the next item into n, n_qt, fresh, release
+        const Item *ip = rd.get<32>(sItem, item_full, epoch, 15);
+        if (!ip) return false;
+        n_qt = uniform(ip->n_qt);
+        n = uniform(ip->n_kv);
+        fresh = !resident || uniform(ip->fresh);
+        release = !resident || uniform(ip->release);
+        rd.done(item_empty, lane);
+        return true;
+      };
+      // S of an item's first step: waits for its Q, and its K if new
+      auto first_s = [&](const Ring<NS> &rg) -> bool {
+        const uint32_t qs = X * QB + qc % QB;
+        const int st = rg.stage(resident, 0);
+        if (!warp_wait<32>(q_full + qs, (qc / QB) & 1, epoch, 3)) return false;
+        if (fresh && !warp_wait<32>(k_full + st, rg.phase(resident, 0), epoch, 4)) return false;
+        tc_fence_after();
+        if (leader) {
+          issue_s(qs, st);
+          // the stage is handed back at the last item that reads it
+          if (release) tc_commit(k_empty + st);
+          if (n == 1) tc_commit(q_empty + qs);
+        }
+        __syncwarp();
+        return true;
+      };
+      bool primed = false;                             // S of the item's first step is issued
+      ok = fetch();
+      while (ok && n_qt > 0) {
+        const int cn = n;
+        const bool cfresh = fresh, crel = release, here = X < n_qt && n > 0;
+        if (here && !primed && !(ok = first_s(ring))) break;
+        primed = false;
+        const uint32_t qs = X * QB + qc % QB;
+        if (here) ++qc;
+        Ring<NS> next_ring = ring;                     // position of the next item
+        if (resident) next_ring.run += crel;
+        else next_ring.pos += cn;
+        if (here) {
+          for (int j = 0; j < cn; ++j, ++steps) {
+            const bool more = j + 1 < cn;
+            const int st = ring.stage(resident, j), st1 = ring.stage(resident, j + 1);
+            if (cfresh) {
+              if (!(ok = warp_wait<32>(v_ready + st, ring.phase(resident, j), epoch, 5))) break;
+              if (more && !(ok = warp_wait<32>(k_full + st1, ring.phase(resident, j + 1), epoch, 4))) break;
+            }
+            if (!more && !(ok = fetch())) break;       // n, n_qt, fresh, release: now the next item's
+            if (!(ok = warp_wait<32>(p_full + X, steps & 1, epoch, 7))) break;
+            tc_fence_after();
+            if (leader) {
               const uint32_t va = aV + st * K::VTILE;
 #pragma unroll
               for (int kk = 0; kk < BN / 16; ++kk)
                 mma_ts(dO, dS + kk * 8, sdesc<K::VAT, 8 * K::VSW, layout_of(K::VSW)>(va + kk * 16 * K::VSW), IDPV,
                        (j > 0 || kk > 0) ? 1u : 0u);
-              if (release) tc_commit(v_empty + st);
+              if (more) {
+                issue_s(qs, st1);                      // over P(j), which PV(j) has read by then
+                if (crel) {
+                  tc_commit(v_empty + st);
+                  tc_commit(k_empty + st1);
+                }
+                if (j + 2 == cn) tc_commit(q_empty + qs);
+              } else {
+                tc_commit(o_full + X);
+                if (crel) tc_commit(v_empty + st);
+              }
             }
-            if (!ok) break;
-            tc_commit(o_full + X);
-            ++oc;
+            __syncwarp();
           }
-          // stages this tile did not use in this item: hand them back once they
-          // were filled (a commit: earlier items of the run may still read them)
-          if (release) {
-            const int n = resident ? a.max_steps : it.n_kv;
-            for (int j = X < it.n_qt ? it.n_kv : 0; j < n && ok; ++j) {
-              const int st = ring.stage(resident, j);
-              const uint32_t ph = ring.phase(resident, j);
-              if (!(ok = mbar_wait(k_full + st, ph, epoch, 8))) break;
+          if (!ok) break;
+          // straight on to the next item
+          if (X < n_qt && n > 0) {
+            if (!(ok = first_s(next_ring))) break;
+            primed = true;
+          }
+        }
+        // stages this tile did not use in this item: hand them back once they
+        // were filled (a commit: earlier items of the run may still read them)
+        if (crel) {
+          const int last = resident ? a.max_steps : cn;
+          for (int j = here ? cn : 0; j < last && ok; ++j) {
+            const int st = ring.stage(resident, j);
+            const uint32_t ph = ring.phase(resident, j);
+            if (!(ok = warp_wait(k_full + st, ph, epoch, 8))) break;
+            if (!(ok = warp_wait(v_ready + st, ph, epoch, 9))) break;
+            if (leader) {
               tc_commit(k_empty + st);
-              if (!(ok = mbar_wait(v_ready + st, ph, epoch, 9))) break;
               tc_commit(v_empty + st);
             }
-            if (resident) ++ring.run;
-            else ring.pos += it.n_kv;
+            __syncwarp();
           }
-          if (it.n_kv > 0) qc += it.n_qt;
-          it = nx;
         }
-        // every MMA issued by this thread completes before TMEM is released
+        if (!here && ok) ok = fetch();
+        ring = next_ring;
+      }
+      // every MMA issued completes before TMEM is released
+      __syncwarp();
+      if (leader) {
         tc_commit(mma_done + X);
         mbar_drain(mma_done + X, 0);
+      }
+      __syncwarp();
+    } else if (warp == K::W_SCHED) {
+      // ================= scheduler =================
+      if (lane == 0) {
+        Walk<D> wk(a);
+        Item it;
+        if (wk.x < wk.end) it = decode<D>(a, sSet, wk.x);
+        else it.n_qt = 0;
+        it.fresh = 1;
+        for (uint32_t i = 0;; ++i) {
+          Item nx = it;
+          if (it.n_qt > 0) nx = wk.after(a, sSet, it);
+          it.release = it.n_qt > 0 && (nx.n_qt == 0 || nx.fresh);
+          if (!mbar_wait(item_empty + i % ITEMS, ((i / ITEMS) & 1) ^ 1, epoch, 16)) break;
+          sItem[i % ITEMS] = it;
+          mbar_arrive(item_full + i % ITEMS);
+          if (it.n_qt == 0) break;
+          it = nx;
+          wk.x += wk.inc;
+        }
       }
       __syncwarp();
     } else if (warp == K::W_FIX) {
@@ -681,14 +838,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       constexpr int A1 = K::ONES ? D / K::VW : 0, XB = (D % K::VW) * 2;
       bool ok = true;
       Ring<NS> ring;
-      Walk wk(a);
-      Item prev;
+      Reader rd;
       bool first = true;
-      for (int x = wk.x; x < wk.end && ok; x += wk.inc) {
-        const Item it = decode<D>(a, sSet, x);
-        if (resident && !first && same_keys(prev, it)) continue;
+      while (ok) {
+        const Item *ip = rd.get<0>(sItem, item_full, epoch, 15);
+        if (!ip) break;
+        const Item it = *ip;
+        rd.done(item_empty, lane);
+        if (it.n_qt == 0) break;
+        if (resident && !it.fresh) continue;
         if (resident && !first) ++ring.run;
-        prev = it;
         first = false;
         const int n = resident ? a.max_steps : it.n_kv;
         for (int j = 0; j < n; ++j) {
@@ -732,21 +891,26 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (!resident) ring.pos += it.n_kv;
       }
     }
-  } else if (warp < 4 * NT) {
+  } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(K::R_SOFT));
-    // ================= softmax warpgroups =================
+    // ================= softmax and epilogue of tile X =================
     const int X = warp >> 2;                   // tile
     const int r = ((warp & 3) << 5) + lane;    // row in tile == TMEM lane
     const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + X * K::TW;
     const uint32_t tO = tS + BN;
     const float sl2 = a.scale_log2;
     const float2 scale2 = make_float2(sl2, sl2);
+    uint8_t *stg = sStg + warp * K::STG;
     uint32_t gs = 0, oc = 0;                   // steps and items of this tile
     bool ok = true;
-    Walk wk(a);
-    for (int x = wk.x; x < wk.end && ok; x += wk.inc) {
-      const Item it = decode<D>(a, sSet, x);
-      if (X >= it.n_qt || it.n_kv <= 0) continue;
+    Reader rd;
+    while (ok) {
+      const Item *ip = rd.get<8>(sItem, item_full, epoch, 15);
+      if (!ip) break;
+      const Item it = *ip;
+      rd.done(item_empty, lane);
+      if (it.n_qt == 0) break;
+      if (X >= it.n_qt) continue;
       float m = NO_KEY, l = 0.f;
       for (int j = 0; j < it.n_kv; ++j, ++gs) {
         const Step sp = step_of<BN>(it, j);
@@ -759,7 +923,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           for (int i = 0; i < BN / 32; ++i)
             live[i] = __ballot_sync(0xffffffffu, 32 * i + lane < sp.valid && (!mk || st::after_wait(mk)[32 * i + lane]));
         }
-        if (!(ok = mbar_wait<8>(s_full + X, gs & 1, epoch, 11))) break;
+        if (!(ok = warp_wait<8>(s_full + X, gs & 1, epoch, 11))) break;
         tc_fence_after();
         uint32_t sr[BN];
 #pragma unroll
@@ -838,149 +1002,104 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         mbar_arrive(p_full + X);
       }
       if (!ok) break;
-      // hand the row statistics to the epilogue warpgroup
-      if (!(ok = mbar_wait(stat_empty + X, (oc & 1) ^ 1, epoch, 12))) break;
-      sStat[(X * 2 + 0) * BLOCK_M + r] = m;
-      sStat[(X * 2 + 1) * BLOCK_M + r] = l;
-      mbar_arrive(stat_full + X);
-      ++oc;
-    }
-  } else {
-    if constexpr (K::R_EPI < K::R_LAUNCH) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K::R_EPI));
-    // ================= epilogue warpgroup =================
-    const int qd = warp - K::W_EPI;            // TMEM lane quadrant
-    const int r = qd * 32 + lane;
-    uint8_t *stg = sStg + qd * K::STG;
-    uint32_t oc[NT];
-#pragma unroll
-    for (int X = 0; X < NT; ++X) oc[X] = 0;
-    bool ok = true;
-    Walk wk(a);
-    for (int x = wk.x; x < wk.end && ok; x += wk.inc) {
-      const Item it = decode<D>(a, sSet, x);
-      int c3 = 0, c4 = 0;
-      if (a.tma_out) {
-        const int b = int(st::fdiv(uint32_t(it.unit), a.dt)), t = it.unit - b * a.c.g.T;
-        if (a.c.g.tblk != a.c.g.T) {
-          c3 = t % a.c.g.tblk;
-          c4 = b * (a.c.g.T / a.c.g.tblk) + t / a.c.g.tblk;
-        } else {
-          c3 = t;
-          c4 = b;
-        }
+      // O of the item: divided by the row sum, written out.  P of the next item
+      // follows in this warp, so its PV cannot overwrite O before it is read.
+      const int row = it.r0 + X * a.tile_rows + r;           // row of the unit
+      const bool valid = r < a.tile_rows && row < a.c.R;
+      const bool some = it.n_kv > 0;
+      float inv = 0.f, lse = -INFINITY;
+      if (some) {
+        if (!(ok = warp_wait<8>(o_full + X, oc & 1, epoch, 13))) break;
+        ++oc;
+        tc_fence_after();
       }
+      const long long prow = (long long)it.split * a.c.part_rows + ((long long)it.unit * a.c.HW + it.w) * a.c.R + row;
+      const long long off = a.tma_out || !valid ? 0 : (a.c.part_o ? prow * D : st::cond_row(a.c, it.unit, it.w, row));
+      const int row0 = it.r0 + X * a.tile_rows + (warp & 3) * 32;
+      // O leaves TMEM from its last columns (which may hold the row sum), GRP
+      // chunks of 16 at a time
+      constexpr int NCH = (D + 15) / 16, GRP = D == 128 ? 4 : (D == 96 ? 3 : NCH);
 #pragma unroll
-      for (int X = 0; X < NT; ++X) {
-        if (X >= it.n_qt || !ok) continue;
-        const int row = it.r0 + X * a.tile_rows + r;         // row of the unit
-        const bool valid = r < a.tile_rows && row < a.c.R;
-        float inv = 0.f, lse = -INFINITY;
-        const uint32_t tO = tmem + ((uint32_t)(qd * 32) << 16) + X * K::TW + BN;
-        const bool some = it.n_kv > 0;
+      for (int c0 = NCH; c0 > 0; c0 -= GRP) {
+        uint32_t ov[GRP][16];
+#pragma unroll
+        for (int i = 0; i < GRP; ++i)
+          if (c0 - 1 - i >= 0) {
+            if (some) COND_LD16(tO + (c0 - 1 - i) * 16, ov[i]);
+            else
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ov[i][e] = 0u;
+          }
         if (some) {
-          if (!(ok = mbar_wait(o_full + X, oc[X] & 1, epoch, 13))) continue;
-          if (!(ok = mbar_wait(stat_full + X, oc[X] & 1, epoch, 14))) continue;
-          ++oc[X];
-          tc_fence_after();
-          const float m = sStat[(X * 2 + 0) * BLOCK_M + r];
-          float l = sStat[(X * 2 + 1) * BLOCK_M + r];
-          mbar_arrive(stat_empty + X);
-          if constexpr (K::ONES) {             // the sum of the bf16 weights
-            uint32_t t[16];
-            COND_LD16(tO + D / 16 * 16, t);
-            tmem_wait_ld();
-            l = __uint_as_float(t[D % 16]);
-          }
-          if (m > NO_KEY || l != l) {          // else no key counted: o = 0, lse = -inf
-            inv = 1.0f / l;
-            lse = (m + log2f(l)) * 0.6931471805599453f;
-          }
-        }
-        const long long prow = (long long)it.split * a.c.part_rows + ((long long)it.unit * a.c.HW + it.w) * a.c.R + row;
-        const bool direct = !a.tma_out;
-        const long long off = !direct || !valid ? 0 : (a.c.part_o ? prow * D : st::cond_row(a.c, it.unit, it.w, row));
-        if (a.tma_out) {
-          if (lane == 0) bulk_wait_read();     // the previous tile's store has read the staging rows
-          __syncwarp();
-        }
-#pragma unroll
-        for (int c = 0; c < D; c += 16) {      // 16 columns at a time; the last may be partly padding
-          uint32_t ov[16];
-          if (some) {
-            COND_LD16(tO + c, ov);
-            tmem_wait_ld();
-            if (c + 16 >= D) {
-              tc_fence_before();
-              mbar_arrive(o_empty + X);        // O of this tile may be overwritten
+          tmem_wait_ld();
+          if (c0 == NCH) {
+            if constexpr (K::ONES) l = __uint_as_float(ov[0][D % 16]);   // the sum of the bf16 weights
+            if (m > NO_KEY || l != l) {      // else no key counted: o = 0, lse = -inf
+              inv = __fdividef(1.0f, l);
+              lse = (m + __log2f(l)) * 0.6931471805599453f;
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) ov[e] = 0u;
           }
+        }
+        if (a.tma_out) {
+          if (c0 == NCH) {
+            if (lane == 0) bulk_wait_read(); // the previous tile's store has read the staging rows
+            __syncwarp();
+          }
+          if (D == 128 && c0 == 4) {         // one 128-byte chunk of staging: the upper half goes out first
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (row0 < a.c.R) tma_store_5d(&mp.o1, stg, 64, it.w, row0, it.c3, it.c4);
+              bulk_commit();
+              bulk_wait_read();
+            }
+            __syncwarp();
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < GRP; ++i) {
+          const int c = (c0 - 1 - i) * 16;
+          if (c < 0) continue;
           float y[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = inv == 0.f ? 0.f : __uint_as_float(ov[e]) * inv;
-          if (direct) {
-            if (valid) {
-              // a part without keys is not read by the combine kernel
-              if (a.c.part_o || a.c.o_f32) {
-                float *dst = (a.c.part_o ? a.c.part_o : static_cast<float *>(a.c.o)) + off + c;
+          for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(ov[i][e]) * inv;
+          if (!a.tma_out && valid && (a.c.part_o || a.c.o_f32)) {
+            // a part without keys is not read by the combine kernel
+            float *dst = (a.c.part_o ? a.c.part_o : static_cast<float *>(a.c.o)) + off + c;
 #pragma unroll
-                for (int f = 0; f < 4; ++f)
-                  if (c + 4 * f < D)
-                    *reinterpret_cast<float4 *>(dst + 4 * f) = make_float4(y[4 * f], y[4 * f + 1], y[4 * f + 2], y[4 * f + 3]);
-              } else {
-                uint16_t *dst = static_cast<uint16_t *>(a.c.o) + off + c;
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-                  if (c + 8 * f < D)
-                    *reinterpret_cast<uint4 *>(dst + 8 * f) =
-                        make_uint4(st::pack_bf16x2(y[8 * f], y[8 * f + 1]), st::pack_bf16x2(y[8 * f + 2], y[8 * f + 3]),
-                                   st::pack_bf16x2(y[8 * f + 4], y[8 * f + 5]), st::pack_bf16x2(y[8 * f + 6], y[8 * f + 7]));
-              }
-            }
-          } else {
-            const bool lo = c < K::C0;         // which part of the head's channels
-            const int f0 = (lo ? c : c - K::C0) / 8;
-            if (D == 128 && c == 64) {         // one 128-byte chunk of staging: the first half goes out first
-              fence_async_smem();
-              __syncwarp();
-              const int row0 = it.r0 + X * a.tile_rows + qd * 32;
-              if (lane == 0) {
-                if (row0 < a.c.R) tma_store_5d(&mp.o0, stg, 0, it.w, row0, c3, c4);
-                bulk_commit();
-                bulk_wait_read();
-              }
-              __syncwarp();
-            }
-            uint8_t *rowp = D == 128 || lo ? stg + lane * K::SW0 : stg + 32 * K::SW0 + lane * K::SW1X;
+            for (int f = 0; f < 4; ++f)
+              if (c + 4 * f < D)
+                *reinterpret_cast<float4 *>(dst + 4 * f) = make_float4(y[4 * f], y[4 * f + 1], y[4 * f + 2], y[4 * f + 3]);
+          }
+          if (a.tma_out || (valid && !a.c.part_o && !a.c.o_f32)) {
+            // staged in the swizzle of the store's part of the head, or straight to the row
+            const bool lo = D == 128 || c < K::C0;
+            const int f0 = (c < K::C0 ? c : c - K::C0) / 8;
+            uint8_t *rowp = lo ? stg + lane * K::SW0 : stg + 32 * K::SW0 + lane * K::SW1X;
+            uint16_t *dst = static_cast<uint16_t *>(a.c.o) + off + c;
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
-              const int at = D == 128 || lo ? swz<K::SW0>(lane, f0 + f) : swz<K::SW1X>(lane, f0 + f);
-              *reinterpret_cast<uint4 *>(rowp + (at << 4)) =
-                  make_uint4(st::pack_bf16x2(y[8 * f], y[8 * f + 1]), st::pack_bf16x2(y[8 * f + 2], y[8 * f + 3]),
-                             st::pack_bf16x2(y[8 * f + 4], y[8 * f + 5]), st::pack_bf16x2(y[8 * f + 6], y[8 * f + 7]));
+              const int at = lo ? swz<K::SW0>(lane, f0 + f) : swz<K::SW1X>(lane, f0 + f);
+              const uint4 v = make_uint4(st::pack_bf16x2(y[8 * f], y[8 * f + 1]), st::pack_bf16x2(y[8 * f + 2], y[8 * f + 3]),
+                                         st::pack_bf16x2(y[8 * f + 4], y[8 * f + 5]), st::pack_bf16x2(y[8 * f + 6], y[8 * f + 7]));
+              if (a.tma_out) *reinterpret_cast<uint4 *>(rowp + (at << 4)) = v;
+              else if (c + 8 * f < D) *reinterpret_cast<uint4 *>(dst + 8 * f) = v;
             }
           }
         }
-        if (a.tma_out) {
-          fence_async_smem();
-          __syncwarp();
-          const int row0 = it.r0 + X * a.tile_rows + qd * 32;
-          if (lane == 0 && row0 < a.c.R) {
-            if (D == 128) {
-              tma_store_5d(&mp.o1, stg, 64, it.w, row0, c3, c4);
-            } else {
-              tma_store_5d(&mp.o0, stg, 0, it.w, row0, c3, c4);
-              if (K::C1) tma_store_5d(&mp.o1, stg + 32 * K::SW0, 64, it.w, row0, c3, c4);
-            }
-            bulk_commit();
-          }
+      }
+      if (a.tma_out) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && row0 < a.c.R) {
+          tma_store_5d(&mp.o0, stg, 0, it.w, row0, it.c3, it.c4);
+          if (K::C1 && D != 128) tma_store_5d(&mp.o1, stg + 32 * K::SW0, 64, it.w, row0, it.c3, it.c4);
+          bulk_commit();
         }
-        if (valid) {
-          if (a.c.part_o) a.c.part_lse[prow] = lse;
-          else if (a.c.lse) a.c.lse[st::cond_lse(a.c, it.unit, it.w, row)] = lse;
-        }
+      }
+      if (valid) {
+        if (a.c.part_o) a.c.part_lse[prow] = lse;
+        else if (a.c.lse) a.c.lse[st::cond_lse(a.c, it.unit, it.w, row)] = lse;
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -1108,7 +1227,7 @@ template <int D> st_status launch(const st::CondParams &p, cudaStream_t s) {
   if (regs_ok < 0) {
     cudaFuncAttributes fa;
     if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return ST_ERR_CUDA;
-    regs_ok = fa.numRegs * K::THREADS >= 128 * K::NT * K::R_SOFT + 128 * K::R_EPI + 32 * K::MISC * K::R_MISC ? 1 : 0;
+    regs_ok = fa.numRegs * K::THREADS >= 128 * K::NT * K::R_SOFT + 256 * K::R_MISC ? 1 : 0;
   }
   if (!regs_ok) return ST_ERR_UNSUPPORTED;
   return st::launch_pdl(kern, dim3(ctas), dim3(K::THREADS), K::SMEM, s, m, a);
