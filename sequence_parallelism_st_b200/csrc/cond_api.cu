@@ -27,7 +27,7 @@ using st::KvSeg;
 // prefix are packed.
 constexpr int PACK_ROWS = 32;
 constexpr int MAX_SPLIT = 64;
-constexpr int MIN_STEPS = 4;   // key steps of a part at least
+constexpr int MIN_KEYS = 256;  // keys of a part at least
 
 bool d_supported(int D) { return D == 32 || D == 64 || D == 72 || D == 80 || D == 96 || D == 128; }
 
@@ -153,9 +153,10 @@ st_status make_plan(const st_attn_desc *desc, const st_kv_desc *d0, const st_kv_
   const long long items = (long long)st::cond_units(p) * p.HW * ceil_div(p.R, t.rows);
   const long long cap = (long long)st::device_sms() * (bf16 ? 1 : 2);
   p.n_split = 1;
-  if (with_ws && items * 2 <= cap && steps >= 2 * MIN_STEPS) {
+  const long long min_steps = ceil_div(MIN_KEYS, t.keys);
+  if (with_ws && items * 2 <= cap && steps >= 2 * min_steps) {
     long long n = cap / items;
-    if (n > steps / MIN_STEPS) n = steps / MIN_STEPS;
+    if (n > steps / min_steps) n = steps / min_steps;
     p.n_split = int(n > MAX_SPLIT ? MAX_SPLIT : n);
   }
   pl.workspace = p.n_split > 1 || pack ? size_t(p.n_split) * size_t(p.part_rows) * size_t(g.D + 1) * 4 : 0;

@@ -41,6 +41,7 @@
 
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "cond.cuh"
 
@@ -50,17 +51,18 @@ using st::Geom;
 using st::pdl_trigger;
 using st::pdl_wait;
 
-__device__ unsigned int g_cond_error;        // sites of waits that ran out
+__device__ unsigned int g_cond_error;        // bit of each role whose wait ran out first
 __device__ unsigned int g_cond_abort_epoch;  // launch epoch that must abort
 
 constexpr int BLOCK_M = 128;
-constexpr unsigned long long WAIT_NS = 2000000000ull;  // 2 s per wait
-constexpr int SET_TABLE = 64;                // key ranges of a segment held in shared memory
+constexpr unsigned long long WAIT_NS = 2000000000ull;  // a drain's limit: 2 s
+constexpr uint32_t WAIT_CLOCKS = 3800000000u;          // a wait's: 2 s at 1.9 GHz
 constexpr float NO_KEY = -3.0e38f;           // running max of a row no key counted for yet
 
 template <int D> struct Cfg {
   static constexpr int NT = D <= 96 ? 3 : 2;           // row tiles in flight
-  static constexpr int BN = D <= 96 ? 64 : 128;        // keys per step
+  static constexpr int BN = D <= 64 ? 96 : (D <= 80 ? 80 : (D <= 96 ? 64 : 128));   // keys per step
+  static constexpr int CH = BN / 16;                   // chunks of 16 keys (a K slice of PV)
   static constexpr int C0 = D >= 64 ? 64 : 32;
   static constexpr int R1 = D > 64 ? D - 64 : 0;
   static constexpr int C1 = R1 == 0 ? 0 : (R1 <= 16 ? 16 : (R1 <= 32 ? 32 : 64));
@@ -69,32 +71,40 @@ template <int D> struct Cfg {
   static constexpr int QT0 = BLOCK_M * SW0;
   static constexpr int QTILE = QT0 + BLOCK_M * SW1;
   static constexpr int KT0 = BN * SW0;
-  static constexpr int KTILE = KT0 + BN * SW1;
+  static constexpr int KBYTES = KT0 + BN * SW1, KTILE = (KBYTES + 1023) / 1024 * 1024;   // a 128B swizzle starts at 1 KB
   // V as column atoms of VW elements (MN-major), PV one MMA of N = DPV per 16 keys
   static constexpr int VW = (D == 72 || D == 80) ? 16 : ((D == 96 || D == 32) ? 32 : 64);
   static constexpr int DPV = ((D + VW - 1) / VW) * VW;
   static constexpr int VA = DPV / VW, VSW = VW * 2, VAT = BN * VSW, VTILE = VA * VAT;
+  static_assert(QTILE % 1024 == 0 && VTILE % (8 * VSW) == 0, "swizzle atoms");
   static constexpr bool ONES = DPV > D;
   static constexpr int TW = BN + DPV;                  // TMEM columns of a tile: S (P over it), O
   static_assert(NT * TW <= 512, "TMEM");
-  // Q tiles: QB slots per row tile, its own so that its issuer sees every phase
-  static constexpr int QB = D == 32 ? 2 : 1, NQ = NT * QB;
-  // staging of a warp's 32 rows of O, a 128-byte chunk at a time for head dim 128
-  static constexpr int STG = 32 * (D == 128 ? SW0 : SW0 + SW1);
-  static constexpr int NSTG = NT;                      // one per tile
-  static constexpr int TAIL = 4 * NSTG * STG + 2 * SET_TABLE * 8 + 512 + (NT == 3 ? 1024 : 512);   // + items, barriers
-  static constexpr int NS_RAW = (232448 - 1024 - TAIL - NQ * QTILE) / (KTILE + VTILE);
-  static constexpr int NS = NS_RAW > 8 ? 8 : NS_RAW;   // K/V stages
-  static constexpr int SMEM = 1024 + NQ * QTILE + NS * (KTILE + VTILE) + TAIL;
-  static_assert(SMEM <= 232448 && NS >= 2, "shared memory");
-  // warps: softmax and epilogue of the tiles (4 each), then loader, issuers, V
-  // helper, scheduler; the rest of the last two warpgroups idles
-  static constexpr int W_LOAD = 4 * NT, W_MMA = W_LOAD + 1, W_FIX = W_MMA + NT, W_SCHED = W_FIX + 1;
-  static constexpr int THREADS = 32 * (W_LOAD + 8);
+  // Two Q tiles per row tile, its own so that its issuer sees every phase.  An
+  // item's O is staged over its Q (dead by then) and stored from there, while
+  // the next item's Q is already in the other: rows of 144 and 160 bytes as they
+  // are (16-byte stores of 8 lanes then meet at most 2 to a bank), the other
+  // widths in the layout of Q.
+  static constexpr int QB = 2, NQ = NT * QB;
+  static constexpr bool DENSE = D == 72 || D == 80;
+  static_assert(!DENSE || BLOCK_M * 2 * D <= QTILE, "O over Q");
+  static constexpr int TABLE = D == 128 ? 32 : 64;     // key ranges of a segment held in shared memory
+  static constexpr int TAIL = 2 * TABLE * 8 + 512 + (D == 128 ? 512 : 768);    // key ranges, items, barriers
+  static constexpr int ROOM = 232448 - 1024 - TAIL - NQ * QTILE;
+  // K and V stages: as many of both as fit, at most 8; an odd K tile more
+  static constexpr int NSV = ROOM / (KTILE + VTILE) > 8 ? 8 : ROOM / (KTILE + VTILE);
+  static constexpr int NSK = NSV < 8 && ROOM - NSV * (KTILE + VTILE) >= KTILE ? NSV + 1 : NSV;
+  static constexpr int SMEM = 1024 + NQ * QTILE + NSK * KTILE + NSV * VTILE + TAIL;
+  static_assert(SMEM <= 232448 && NSV >= 1 && NSK >= 2, "shared memory");
+  // warps: softmax and epilogue of the tiles, then loader, issuers, V helper;
+  // the rest of the last two warpgroups idles
+  static constexpr int W_LOAD = 4 * NT, W_MMA = W_LOAD + 1, W_FIX = W_MMA + NT;
+  static constexpr int MISC = NT == 3 ? 8 : 4;
+  static constexpr int THREADS = 32 * (W_LOAD + MISC);
   // registers: granted at launch, then moved to the softmax (setmaxnreg)
-  static constexpr int R_LAUNCH = NT == 3 ? 96 : 128;
-  static constexpr int R_SOFT = NT == 3 ? 120 : 200, R_MISC = 56;
-  static_assert(128 * NT * R_SOFT + 256 * R_MISC <= THREADS * R_LAUNCH, "register split");
+  static constexpr int R_LAUNCH = NT == 3 ? 96 : 168;
+  static constexpr int R_SOFT = NT == 3 ? 120 : 208, R_MISC = NT == 3 ? 56 : 88;
+  static_assert(128 * NT * R_SOFT + 32 * MISC * R_MISC <= THREADS * R_LAUNCH, "register split");
 };
 
 // ---------------------------------------------------------------- exp2
@@ -109,22 +119,32 @@ constexpr float kP0 = 0.9999280571937561f, kP1 = 0.6932609677314758f;
 constexpr float kP2 = 0.2426111251115799f, kP3 = 0.0551716685295105f;
 constexpr int kPolyPairs = 2;                // of every 8 pairs of scores
 
-__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
-      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+// Packed fp32 pairs in 64-bit registers: constants stay in their pair.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float x, float y) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
   return d;
 }
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+__device__ __forceinline__ f32x2 pair(uint32_t x, uint32_t y) { return pair(__uint_as_float(x), __uint_as_float(y)); }
+__device__ __forceinline__ float2 unpair(f32x2 a) {
   float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+  return d;
+}
+__device__ __forceinline__ f32x2 ffma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 fadd2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fmul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
@@ -132,17 +152,18 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ float2 ex2_poly2(float2 x) {
-  x.x = fmaxf(x.x, -125.0f);
-  x.y = fmaxf(x.y, -125.0f);
-  const float2 t = fadd2(x, make_float2(12582912.0f, 12582912.0f));
-  const float2 j = fadd2(t, make_float2(-12582912.0f, -12582912.0f));
-  const float2 f = ffma2(j, make_float2(-1.0f, -1.0f), x);
-  float2 q = ffma2(make_float2(kP3, kP3), f, make_float2(kP2, kP2));
-  q = ffma2(q, f, make_float2(kP1, kP1));
-  q = ffma2(q, f, make_float2(kP0, kP0));
-  return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(t.x) << 23)),
-                     __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
+__device__ __forceinline__ float2 ex2_poly2(f32x2 xx) {
+  float2 x = unpair(xx);
+  const f32x2 c = pair(fmaxf(x.x, -125.0f), fmaxf(x.y, -125.0f));
+  const f32x2 t = fadd2(c, pair(12582912.0f, 12582912.0f));
+  const f32x2 j = fadd2(t, pair(-12582912.0f, -12582912.0f));
+  const f32x2 f = ffma2(j, pair(-1.0f, -1.0f), c);
+  f32x2 q = ffma2(pair(kP3, kP3), f, pair(kP2, kP2));
+  q = ffma2(q, f, pair(kP1, kP1));
+  q = ffma2(q, f, pair(kP0, kP0));
+  const float2 y = unpair(q), tt = unpair(t);
+  return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(tt.x) << 23)),
+                     __int_as_float(__float_as_int(y.y) + (__float_as_int(tt.y) << 23)));
 }
 
 // ---------------------------------------------------------------- PTX helpers
@@ -164,69 +185,44 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // try_wait that suspends the thread until the phase completes or about
 // `hint_ns` nanoseconds pass.
-__device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity, uint32_t hint_ns) {
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+      : "r"(bar), "r"(parity), "r"(hint_ns)
       : "memory");
   return ok != 0;
 }
-// Bounded wait for a phase by one thread: it sleeps in the barrier; the clock
-// and the abort epoch are only consulted after a sleep of ~0.1 ms that ended
-// without the phase.
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint32_t epoch, int site) {
-  if (mbar_test(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer();
-  while (true) {
-    if (mbar_try_wait(bar, parity, 100000u)) return true;
-    if (*reinterpret_cast<volatile unsigned int *>(&g_cond_abort_epoch) == epoch) return false;
-    if (globaltimer() - t0 > WAIT_NS) {
-      atomicOr(&g_cond_error, 1u << (site & 31));
-      atomicExch(&g_cond_abort_epoch, epoch);
+// Bounded wait for a phase: the thread sleeps in the barrier; the clock and the
+// abort epoch are only looked at after a sleep that ended without the phase.
+// A warp that waits does so with all lanes on one barrier, which answers them
+// together.  (Polling before the sleep, and a vote on the answer, each cost the
+// other warps more issue slots than the earlier wake-up gained: 10% and 15% of
+// a launch.)  The limit is counted in SM clocks, WAIT_CLOCKS of them, and what
+// ended is recorded by the caller, once per role: a wait is a few instructions.
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint32_t epoch) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try_wait(b, parity, 100000u)) return true;
+  const uint32_t t0 = uint32_t(clock());
+  while (!mbar_try_wait(b, parity, 100000u))
+    if (*reinterpret_cast<volatile unsigned int *>(&g_cond_abort_epoch) == epoch || uint32_t(clock()) - t0 > WAIT_CLOCKS)
       return false;
-    }
-  }
+  return true;
 }
-// The same by a whole warp, whose lanes agree on the answer (a warp that
-// gives up does so in all lanes).  SPIN polls come first: a polling warp
-// resumes sooner than a suspended one, which the MMA chain notices.
-template <int SPIN = 0>
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t epoch, int site) {
-  for (int i = 0; i <= SPIN; ++i)
-    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-  const unsigned long long t0 = globaltimer();
-  while (true) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity, 100000u))) return true;
-    bool stop = *reinterpret_cast<volatile unsigned int *>(&g_cond_abort_epoch) == epoch;
-    if (globaltimer() - t0 > WAIT_NS) {
-      atomicOr(&g_cond_error, 1u << (site & 31));
-      atomicExch(&g_cond_abort_epoch, epoch);
-      stop = true;
-    }
-    if (__any_sync(0xffffffffu, stop)) return false;
-  }
+// A wait of this role gave up: the first one of a launch is recorded, and the
+// launch's other waits end.
+__device__ __forceinline__ void gave_up(uint32_t epoch, int role) {
+  if (atomicExch(&g_cond_abort_epoch, epoch) != epoch) atomicOr(&g_cond_error, 1u << role);
 }
 // The same for the end of work already issued, whatever the abort epoch.
 __device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {
   const unsigned long long t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity, 100000u) && globaltimer() - t0 < WAIT_NS) {
+  while (!mbar_try_wait(smem_u32(bar), parity, 100000u) && globaltimer() - t0 < WAIT_NS) {
   }
 }
 
@@ -262,27 +258,35 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
-}
-// D[tmem] (+)= A[smem] * B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The MMA and commit instructions are issued by the lane whose `lead` is set,
+// by predicate instead of a branch: the control flow around them stays
+// uniform, so descriptors are computed on the uniform datapath.
+__device__ __forceinline__ void tc_commit(uint32_t lead, uint64_t *bar) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
 #define COND_LD16(taddr, r)                                                                                          \
@@ -297,16 +301,28 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
                  "r"((r)[6]), "r"((r)[7]), "r"((r)[8]), "r"((r)[9]), "r"((r)[10]), "r"((r)[11]), "r"((r)[12]),        \
                  "r"((r)[13]), "r"((r)[14]), "r"((r)[15])                                                             \
                : "memory")
+#define COND_LD8(taddr, r)                                                                                            \
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"                                \
+               : "=r"((r)[0]), "=r"((r)[1]), "=r"((r)[2]), "=r"((r)[3]), "=r"((r)[4]), "=r"((r)[5]), "=r"((r)[6]),    \
+                 "=r"((r)[7])                                                                                         \
+               : "r"(taddr))
+#define COND_ST8(taddr, r)                                                                                            \
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"((r)[0]),      \
+               "r"((r)[1]), "r"((r)[2]), "r"((r)[3]), "r"((r)[4]), "r"((r)[5]), "r"((r)[6]), "r"((r)[7])              \
+               : "memory")
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory matrix descriptor: start address, leading and stride byte
-// offsets, version 1, swizzle layout 2 = 128B, 4 = 64B, 6 = 32B.
-template <uint32_t LBO, uint32_t SBO, uint32_t LAYOUT>
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr) {
+// offsets, version 1, swizzle layout 2 = 128B, 4 = 64B, 6 = 32B.  The low word
+// is the start address in 16-byte units (14 bits hold all of shared memory)
+// and the leading offset, so later operands of a tile are an addition away.
+template <uint32_t LBO> __device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr) {
+  return (saddr >> 4) | (((LBO >> 4) & 0x3FFFu) << 16);
+}
+template <uint32_t SBO, uint32_t LAYOUT> __device__ __forceinline__ uint64_t sdesc(uint32_t lo) {
   constexpr uint32_t hi = ((SBO >> 4) & 0x3FFFu) | (1u << 14) | (LAYOUT << 29);
-  constexpr uint32_t lo = ((LBO >> 4) & 0x3FFFu) << 16;
-  return ((uint64_t)hi << 32) | (uint64_t)(((saddr >> 4) & 0x3FFFu) | lo);
+  return ((uint64_t)hi << 32) | lo;
 }
 __host__ __device__ constexpr uint32_t layout_of(int swizzle_bytes) {
   return swizzle_bytes == 128 ? 2u : (swizzle_bytes == 64 ? 4u : 6u);
@@ -319,14 +335,14 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
 // Lane 0's value, known to the compiler to be the same in the whole warp.
 template <typename T> __device__ __forceinline__ T uniform(T v) { return T(__shfl_sync(0xffffffffu, v, 0)); }
 // True in one lane of the converged warp, always the same one.
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "elect.sync _|p, 0xffffffff;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(ok));
-  return ok != 0;
+  return ok;
 }
 // 16-byte chunk f of row r of a swizzled tile with rows of `bytes`.
 template <int BYTES> __device__ __forceinline__ int swz(int r, int f) {
@@ -342,8 +358,13 @@ struct Maps {
 
 struct Args {
   st::CondParams c;
-  st::FastDiv dqb, dsplit, dhw, dkv, dt, dper[2];
+  st::FastDiv dqb, dsplit, dhw, dkv, dt, dtblk, dper[2];
+  int n_tblk;                  // frame blocks of a batch
   int q_blocks, tile_rows;     // row blocks of a unit, rows of a tile (128, or whole groups of heads)
+  // Resident: the row blocks are cut into bands of `band` (the last one
+  // `band_last`), and items run through all heads and units within a band
+  int band, band_last, cols, n_bands;
+  st::FastDiv dband, dband_last, dbandcols;
   int n_items;
   int resident;                // every key tile of an item fits the ring: K and V stay from item to item
   int max_steps;
@@ -365,8 +386,8 @@ struct alignas(16) Item {
   int kvh;
   int fresh;                   // its keys are not those of the item before
   int release;                 // nor those of the item after
-  int qb;                      // row block of the unit
-  int pad[4];
+  int qb, qb_end;              // row block of the unit; end of its band
+  int pad[3];
 };
 constexpr int ITEMS = 4;       // items in flight between the scheduler and the others
 static_assert(ITEMS * sizeof(Item) <= 512, "item ring");
@@ -393,23 +414,38 @@ template <int D> __device__ __forceinline__ void rows_of(const Args &a, Item &it
   it.n_qt = left > 2 * a.tile_rows && Cfg<D>::NT > 2 ? 3 : (left > a.tile_rows ? 2 : 1);
 }
 
-// q block fastest, then split, head, unit.  table: the segments' key ranges (row, n).
+// Streaming: q block fastest, then split, head, unit.  Resident: q block of a
+// band, head and unit, band.  table: the segments' key ranges (row, n).
 template <int D>
 __device__ __forceinline__ Item decode(const Args &a, const int2 *table, int x) {
   using K = Cfg<D>;
   Item it;
-  const uint32_t y = st::fdiv(uint32_t(x), a.dqb);
-  it.qb = x - int(y) * a.q_blocks;
-  const uint32_t z = st::fdiv(y, a.dsplit);
-  it.split = int(y) - int(z) * a.c.n_split;
+  uint32_t z;                                  // unit * HW + walked head
+  if (a.resident) {
+    const int band = int(st::fdiv(uint32_t(x), a.dbandcols));
+    const bool last = band + 1 >= a.n_bands;
+    const int len = last ? a.band_last : a.band;
+    x -= band * a.band * a.cols;
+    z = st::fdiv(uint32_t(x), last ? a.dband_last : a.dband);
+    it.qb = band * a.band + x - int(z) * len;
+    it.qb_end = band * a.band + len;
+    it.split = 0;
+  } else {
+    const uint32_t y = st::fdiv(uint32_t(x), a.dqb);
+    it.qb = x - int(y) * a.q_blocks;
+    it.qb_end = a.q_blocks;
+    z = st::fdiv(y, a.dsplit);
+    it.split = int(y) - int(z) * a.c.n_split;
+  }
   it.unit = int(st::fdiv(z, a.dhw));
   it.w = int(z) - it.unit * a.c.HW;
   it.kvh = int(st::fdiv(uint32_t(it.w), a.dkv));
   rows_of<D>(a, it);
   const int ub = int(st::fdiv(uint32_t(it.unit), a.dt)), t = it.unit - ub * a.c.g.T;
   if (a.c.g.tblk != a.c.g.T) {
-    it.c3 = t % a.c.g.tblk;
-    it.c4 = ub * (a.c.g.T / a.c.g.tblk) + t / a.c.g.tblk;
+    const int tb = int(st::fdiv(uint32_t(t), a.dtblk));
+    it.c3 = t - tb * a.c.g.tblk;
+    it.c4 = ub * a.n_tblk + tb;
   } else {
     it.c3 = t;
     it.c4 = ub;
@@ -419,8 +455,8 @@ __device__ __forceinline__ Item decode(const Args &a, const int2 *table, int x) 
     set = row = n = 0;
     if (g >= a.c.n_seg) return;
     set = int(st::fdiv(uint32_t(b), a.dper[g]));
-    if (a.c.seg[g].n_sets <= SET_TABLE) {
-      const int2 r = table[g * SET_TABLE + set];
+    if (a.c.seg[g].n_sets <= K::TABLE) {
+      const int2 r = table[g * K::TABLE + set];
       row = r.x;
       n = r.y;
     } else {
@@ -447,34 +483,32 @@ __device__ __forceinline__ bool same_keys(const Item &a, const Item &b) {
   return a.kvh == b.kvh && a.set0 == b.set0 && a.set1 == b.set1;
 }
 
-// The items of a CTA: consecutive ones when K and V stay resident, else every
-// gridDim-th, so that the CTAs that run together share K/V tiles in L2.  The
-// next row block of the same keys needs no division.
-template <int D> struct Walk {
+// The items of a CTA.  Streaming: every gridDim-th, so that the CTAs that run
+// together share K/V tiles in L2.  Resident: consecutive ones, a band of row
+// blocks of one head; the next row block needs no division.  The CTAs beside
+// work on the same rows of the other heads, whose channels lie next to these
+// in Q and O: sectors that two heads share, and DRAM pages, are then touched
+// at about the same time.  (Heads at different rows at a time: Q and O of
+// 65,536 x 16 heads x 72 ran at 2.3 TB/s.)
+struct Walk {
   int x, end, inc;
   __device__ __forceinline__ explicit Walk(const Args &a) {
     if (a.resident) {
-      x = int((long long)a.n_items * blockIdx.x / gridDim.x);
-      end = int((long long)a.n_items * (blockIdx.x + 1) / gridDim.x);
       inc = 1;
+      if (int(gridDim.x) >= a.n_bands * a.cols) {      // a band of a head per CTA
+        const int band = int(blockIdx.x) / a.cols, col = int(blockIdx.x) - band * a.cols;
+        const int len = band + 1 < a.n_bands ? a.band : a.band_last;
+        x = band * a.band * a.cols + col * len;
+        end = band < a.n_bands ? x + len : x;
+      } else {
+        x = int((long long)a.n_items * blockIdx.x / gridDim.x);
+        end = int((long long)a.n_items * (blockIdx.x + 1) / gridDim.x);
+      }
     } else {
       x = blockIdx.x;
       end = a.n_items;
       inc = gridDim.x;
     }
-  }
-  __device__ __forceinline__ Item after(const Args &a, const int2 *table, const Item &it) const {
-    Item nx = it;
-    if (x + inc >= end) {
-      nx.n_qt = 0;
-    } else if (inc == 1 && it.qb + 1 < a.q_blocks) {
-      ++nx.qb;
-      rows_of<D>(a, nx);
-    } else {
-      nx = decode<D>(a, table, x + inc);
-    }
-    nx.fresh = !same_keys(it, nx);
-    return nx;
   }
 };
 
@@ -483,9 +517,8 @@ struct Reader {
   uint32_t i = 0;
   // The next item, once it is there: the caller reads what it needs, then the
   // warp hands it back.
-  template <int SPIN>
-  __device__ __forceinline__ const Item *get(const Item *items, uint64_t *full, uint32_t epoch, int site) const {
-    return warp_wait<SPIN>(full + i % ITEMS, (i / ITEMS) & 1, epoch, site) ? items + i % ITEMS : nullptr;
+  __device__ __forceinline__ const Item *get(const Item *items, uint64_t *full, uint32_t epoch) const {
+    return mbar_wait(full + i % ITEMS, (i / ITEMS) & 1, epoch) ? items + i % ITEMS : nullptr;
   }
   __device__ __forceinline__ void done(uint64_t *empty, int lane) {
     __syncwarp();
@@ -496,10 +529,12 @@ struct Reader {
 
 // Position of the K/V ring: streaming, steps follow one another; resident,
 // step j is in stage j and `run` counts the loads of each.
-template <int NS> struct Ring {
+struct Ring {
   uint32_t pos = 0, run = 0;
-  __device__ __forceinline__ int stage(bool resident, int j) const { return resident ? j : int((pos + j) % NS); }
-  __device__ __forceinline__ uint32_t phase(bool resident, int j) const {
+  template <int NS> __device__ __forceinline__ int stage(bool resident, int j) const {
+    return resident ? j : int((pos + j) % NS);
+  }
+  template <int NS> __device__ __forceinline__ uint32_t phase(bool resident, int j) const {
     return (resident ? run : (pos + j) / NS) & 1;
   }
 };
@@ -508,21 +543,21 @@ template <int D>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     cond_attn_sm100(const __grid_constant__ Maps mp, const __grid_constant__ Args a) {
   using K = Cfg<D>;
-  constexpr int NT = K::NT, NS = K::NS, NQ = K::NQ, QB = K::QB, BN = K::BN;
+  constexpr int NT = K::NT, NSK = K::NSK, NSV = K::NSV, NQ = K::NQ, QB = K::QB, BN = K::BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sQ = base;
   uint8_t *sK = sQ + NQ * K::QTILE;
-  uint8_t *sV = sK + NS * K::KTILE;
-  uint8_t *sStg = sV + NS * K::VTILE;
-  int2 *sSet = reinterpret_cast<int2 *>(sStg + 4 * K::NSTG * K::STG);
-  Item *sItem = reinterpret_cast<Item *>(sSet + 2 * SET_TABLE);
+  uint8_t *sV = sK + NSK * K::KTILE;
+  int2 *sSet = reinterpret_cast<int2 *>(sV + NSV * K::VTILE);
+  Item *sItem = reinterpret_cast<Item *>(sSet + 2 * K::TABLE);
   uint64_t *bars = reinterpret_cast<uint64_t *>(sItem + ITEMS);
   uint64_t *q_full = bars, *q_empty = q_full + NQ;
-  uint64_t *k_full = q_empty + NQ, *k_empty = k_full + NS;       // k_empty, v_empty: one arrival per tile
-  uint64_t *v_full = k_empty + NS, *v_empty = v_full + NS, *v_ready = v_empty + NS;
-  uint64_t *s_full = v_ready + NS, *p_full = s_full + NT;
-  uint64_t *o_full = p_full + NT, *mma_done = o_full + NT;
+  uint64_t *k_full = q_empty + NQ, *k_empty = k_full + NSK;      // k_empty, v_empty: one arrival per tile
+  uint64_t *v_full = k_empty + NSK, *v_empty = v_full + NSV, *v_ready = v_empty + NSV;
+  // per tile: S ready; P written; O of an item complete
+  uint64_t *s_full = v_ready + NSV, *p_full = s_full + NT, *o_full = p_full + NT;
+  uint64_t *mma_done = o_full + NT;
   uint64_t *item_full = mma_done + NT, *item_empty = item_full + ITEMS;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(item_empty + ITEMS);
 
@@ -530,11 +565,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NQ; ++i) {
       mbar_init(q_full + i, 1);
-      mbar_init(q_empty + i, 1);
+      mbar_init(q_empty + i, 4);             // the softmax warps, once O is out of it
     }
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < NSK; ++i) {
       mbar_init(k_full + i, 1);
       mbar_init(k_empty + i, NT);
+    }
+    for (int i = 0; i < NSV; ++i) {
       mbar_init(v_full + i, 1);
       mbar_init(v_empty + i, NT);
       mbar_init(v_ready + i, 1);
@@ -547,7 +584,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     }
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_empty + i, 5 * NT + 2);   // softmax warps, issuers, loader, helper
+      mbar_init(item_empty + i, 5 * NT + 1);   // softmax warps, issuers, helper
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -563,12 +600,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   pdl_wait();
 #pragma unroll
   for (int g = 0; g < 2; ++g)
-    if (g < a.c.n_seg && a.c.seg[g].n_sets <= SET_TABLE && int(threadIdx.x) < a.c.seg[g].n_sets) {
+    if (g < a.c.n_seg && a.c.seg[g].n_sets <= K::TABLE && int(threadIdx.x) < a.c.seg[g].n_sets) {
       st::KvSeg sg = a.c.seg[g];
       sg.len = st::after_wait(sg.len);
       sg.offsets = st::after_wait(sg.offsets);
       const st::KvRange r = st::kv_range(sg, int(threadIdx.x) * sg.per);
-      sSet[g * SET_TABLE + threadIdx.x] = make_int2(r.row0, r.n);
+      sSet[g * K::TABLE + threadIdx.x] = make_int2(r.row0, r.n);
     }
   tc_fence_before();
   __syncthreads();
@@ -580,54 +617,76 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   if (warp >= K::W_LOAD) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K::R_MISC));
     if (warp == K::W_LOAD) {
-      // ================= TMA producer =================
-      bool ok = true;
-      Ring<NS> ring;
-      Reader rd;
-      uint32_t qc[NT];                                // Q tiles so far
-#pragma unroll
-      for (int X = 0; X < NT; ++X) qc[X] = 0;
-      int last_kv = -1;                               // streaming: ring position of the last K/V issued
-      int loaded = 0;                                 // resident: stages loaded in this run
-      bool first = true;
-      while (ok) {
-        const Item *ip = rd.get<0>(sItem, item_full, epoch, 15);
-        if (!(ok = ip != nullptr)) break;
-        const Item it = *ip;
-        rd.done(item_empty, lane);
-        if (it.n_qt == 0) break;
-        if (lane == 0) {
+      // ================= scheduler and TMA producer =================
+      // An item is handed out once the next one is known, then loaded.
+      if (lane == 0) {
+        bool ok = true;
+        Ring ring;
+        uint32_t qn = 0;                              // 2 bits per tile: its Q tiles so far (slot, phase)
+        int last_kv = -1;                             // streaming: ring position of the last K/V issued
+        int loaded = 0;                               // resident: stages loaded in this run
+        bool first = true;
+        Walk wk(a);
+        Item sch;                                     // the item to publish
+        sch.n_qt = 1;
+        sch.qb = sch.qb_end = 0;
+        sch.set0 = -1;
+        for (uint32_t i = 0; ok; ++i) {
+          // item i, and whether it has other keys than its neighbours
+          if (sch.n_qt > 0) {
+            const Item prev = sch;
+            if (wk.x >= wk.end) {
+              sch.n_qt = 0;
+            } else if (wk.inc == 1 && sch.qb + 1 < sch.qb_end) {
+              ++sch.qb;
+              rows_of<D>(a, sch);
+            } else {
+              sch = decode<D>(a, sSet, wk.x);
+            }
+            wk.x += wk.inc;
+            sch.fresh = !same_keys(prev, sch);
+            // the item before is complete now: hand it out
+            if (i > 0) {
+              sItem[(i - 1) % ITEMS].release = sch.n_qt == 0 || sch.fresh;
+              mbar_arrive(item_full + (i - 1) % ITEMS);
+            }
+            if (!(ok = mbar_wait(item_empty + i % ITEMS, ((i / ITEMS) & 1) ^ 1, epoch))) break;
+            sItem[i % ITEMS] = sch;
+            if (sch.n_qt == 0) mbar_arrive(item_full + i % ITEMS);
+          }
+          if (i == 0) continue;
+          const Item &it = sItem[(i - 1) % ITEMS];    // its slot is not written again before the next but two
+          if (it.n_qt == 0) break;
           const bool load_kv = !resident || it.fresh;
           if (resident && load_kv && !first) ++ring.run;
           first = false;
           const int n = resident ? (load_kv ? a.max_steps : 1) : it.n_kv;
           for (int j = 0; j < n && ok; ++j) {
-            const int st = ring.stage(resident, j);
-            const uint32_t ph = ring.phase(resident, j);
+            const int sk = ring.stage<NSK>(resident, j), sv = ring.stage<NSV>(resident, j);
             const Step sp = step_of<BN>(it, j);
             const int g = sp.seg;
             const int set = a.c.seg[g].offsets ? 0 : sp.set;   // packed: rows of one long sequence
             const bool real = j < it.n_kv;            // resident: stages past the item's steps only change phase
             if (load_kv) {
-              if (!(ok = mbar_wait(k_empty + st, ph ^ 1, epoch, 1))) break;
+              if (!(ok = mbar_wait(k_empty + sk, ring.phase<NSK>(resident, j) ^ 1, epoch))) break;
               if (real) {
-                mbar_expect_tx(k_full + st, K::KTILE);
-                uint8_t *dk = sK + st * K::KTILE;
-                tma_load_4d(dk, &mp.k0[g], k_full + st, 0, it.kvh, sp.row + sp.key, set);
-                if (K::C1) tma_load_4d(dk + K::KT0, &mp.k1[g], k_full + st, 64, it.kvh, sp.row + sp.key, set);
+                mbar_expect_tx(k_full + sk, K::KBYTES);
+                uint8_t *dk = sK + sk * K::KTILE;
+                tma_load_4d(dk, &mp.k0[g], k_full + sk, 0, it.kvh, sp.row + sp.key, set);
+                if (K::C1) tma_load_4d(dk + K::KT0, &mp.k1[g], k_full + sk, 64, it.kvh, sp.row + sp.key, set);
                 if (!resident) last_kv = int(ring.pos) + j;
                 else loaded = j + 1;
               } else {
-                mbar_arrive(k_full + st);
+                mbar_arrive(k_full + sk);
               }
             }
             if (j == 0 && it.n_kv > 0) {
-#pragma unroll
-              for (int X = 0; X < NT; ++X) {
-                if (X >= it.n_qt || !ok) continue;
-                const int qs = X * QB + qc[X] % QB;
-                if (!(ok = mbar_wait(q_empty + qs, ((qc[X] / QB) & 1) ^ 1, epoch, 0))) continue;
-                ++qc[X];
+#pragma unroll 1
+              for (int X = 0; X < it.n_qt; ++X) {
+                const uint32_t n = qn >> 2 * X & 3;
+                const int qs = X * QB + (n & 1);
+                if (!(ok = mbar_wait(q_empty + qs, (n >> 1) ^ 1, epoch))) break;
+                qn ^= (n ^ ((n + 1) & 3)) << 2 * X;
                 uint8_t *dst = sQ + qs * K::QTILE;
                 const int row = it.r0 + X * a.tile_rows;
                 mbar_expect_tx(q_full + qs, a.tile_rows * (K::SW0 + K::SW1));
@@ -642,207 +701,158 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
               if (!ok) break;
             }
             if (load_kv) {
-              if (!(ok = mbar_wait(v_empty + st, ph ^ 1, epoch, 2))) break;
+              if (!(ok = mbar_wait(v_empty + sv, ring.phase<NSV>(resident, j) ^ 1, epoch))) break;
               if (real) {
-                mbar_expect_tx(v_full + st, K::VTILE);
-                uint8_t *dv = sV + st * K::VTILE;
-#pragma unroll
+                mbar_expect_tx(v_full + sv, K::VTILE);
+                uint8_t *dv = sV + sv * K::VTILE;
+#pragma unroll 1
                 for (int t = 0; t < K::VA; ++t)
-                  tma_load_4d(dv + t * K::VAT, &mp.v[g], v_full + st, t * K::VW, it.kvh, sp.row + sp.key, set);
+                  tma_load_4d(dv + t * K::VAT, &mp.v[g], v_full + sv, t * K::VW, it.kvh, sp.row + sp.key, set);
               } else {
-                mbar_arrive(v_full + st);
+                mbar_arrive(v_full + sv);
               }
             }
           }
           if (!resident) ring.pos += it.n_kv;
         }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      }
-      if (!ok && lane == 0) {
-        // the last load issued into every stage and Q slot (a wait for one
-        // that was not issued runs into its limit)
-        if (resident) {
-          for (int j = 0; j < loaded; ++j) {
-            mbar_drain(k_full + j, ring.run & 1);
-            mbar_drain(v_full + j, ring.run & 1);
+        if (!ok) {
+          gave_up(epoch, 0);
+          // the last load issued into every stage and Q slot (a wait for one
+          // that was not issued runs into its limit)
+          if (resident) {
+            for (int j = 0; j < loaded; ++j) {
+              mbar_drain(k_full + j, ring.run & 1);
+              mbar_drain(v_full + j, ring.run & 1);
+            }
+          } else {
+            for (int i = last_kv; i >= 0 && i > last_kv - NSK; --i) mbar_drain(k_full + i % NSK, (i / NSK) & 1);
+            for (int i = last_kv; i >= 0 && i > last_kv - NSV; --i) mbar_drain(v_full + i % NSV, (i / NSV) & 1);
           }
-        } else {
-          for (int i = (last_kv - NS + 1 > 0 ? last_kv - NS + 1 : 0); i <= last_kv; ++i) {
-            mbar_drain(k_full + i % NS, (i / NS) & 1);
-            mbar_drain(v_full + i % NS, (i / NS) & 1);
-          }
+          for (int X = 0; X < NT; ++X)
+            for (uint32_t k = 1; k <= 2; ++k) {       // (a slot never loaded answers at once)
+              const uint32_t n = ((qn >> 2 * X) - k) & 3;
+              mbar_drain(q_full + X * QB + (n & 1), n >> 1);
+            }
         }
-#pragma unroll
-        for (int X = 0; X < NT; ++X)
-          for (int i = (int(qc[X]) > QB ? int(qc[X]) - QB : 0); i < int(qc[X]); ++i)
-            mbar_drain(q_full + X * QB + i % QB, (i / QB) & 1);
       }
       __syncwarp();
     } else if (warp >= K::W_MMA && warp < K::W_MMA + NT) {
       // ================= issuer of tile X =================
       // P of a step ready -> its PV, then S of the next step (of the next item
-      // after the last) into the same columns.  The whole warp walks the loop
-      // and one elected lane issues, so addresses and descriptors stay in
-      // uniform registers: computed by one diverged lane, an MMA took about 200
-      // cycles to issue.
+      // after the last) into the same columns: MMAs of one thread execute in
+      // order.  The whole warp walks the loop.
       const int X = uniform(warp) - K::W_MMA;
-      constexpr uint32_t IDS = idesc_bf16(BLOCK_M, BN, 0, 0), IDPV = idesc_bf16(BLOCK_M, K::DPV, 0, 1);
       const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
       const uint32_t dS = uniform(tmem) + X * K::TW, dO = dS + BN;
-      const bool leader = elect_one();
+      const uint32_t lead = elect_one();
       bool ok = true;
-      Ring<NS> ring;
+      Ring ring;
       Reader rd;
-      uint32_t qc = 0, steps = 0;                      // items and steps of this tile
-      auto issue_s = [&](uint32_t qs, int st) {        // Q in slot qs, K in stage st
-        const uint32_t qa = aQ + qs * K::QTILE, ka = aK + st * K::KTILE;
-#pragma unroll
-        for (int kk = 0; kk < K::C0 / 16; ++kk)
-          mma_ss(dS, sdesc<16, 8 * K::SW0, layout_of(K::SW0)>(qa + kk * 32),
-                 sdesc<16, 8 * K::SW0, layout_of(K::SW0)>(ka + kk * 32), IDS, kk > 0);
-        if (K::C1) {
-#pragma unroll
-          for (int kk = 0; kk < K::C1X / 16; ++kk)
-            mma_ss(dS, sdesc<16, 8 * K::SW1X, layout_of(K::SW1X)>(qa + K::QT0 + kk * 32),
-                   sdesc<16, 8 * K::SW1X, layout_of(K::SW1X)>(ka + K::KT0 + kk * 32), IDS, 1);
+      uint32_t qc = 0, steps = 0;                      // Q tiles and steps of this tile so far
+      struct Work {                                    // what the issuer needs of an item
+        int n_qt, n, n0, n1, s0, j0;
+        bool fresh, release;
+        // chunks of 16 keys of step j
+        __device__ __forceinline__ int chunks(int j) const {
+          j += j0;
+          const int left = j < s0 ? n0 - j * BN : n1 - (j - s0) * BN;
+          return left >= BN ? K::CH : (left + 15) >> 4;
         }
-        tc_commit(s_full + X);
       };
-      int n = 0, n_qt = 0;
-      bool fresh = false, release = false;
-      auto fetch = [&]() -> bool {                     // the next item into n, n_qt, fresh, release
-        const Item *ip = rd.get<32>(sItem, item_full, epoch, 15);
+      Work wk;
+      auto fetch = [&]() -> bool {
+        const Item *ip = rd.get(sItem, item_full, epoch);
         if (!ip) return false;
-        n_qt = uniform(ip->n_qt);
-        n = uniform(ip->n_kv);
-        fresh = !resident || uniform(ip->fresh);
-        release = !resident || uniform(ip->release);
+        wk.n_qt = uniform(ip->n_qt);
+        wk.n = uniform(ip->n_kv);
+        wk.n0 = uniform(ip->n0);
+        wk.n1 = uniform(ip->n1);
+        wk.s0 = uniform(ip->s0);
+        wk.j0 = uniform(ip->j0);
+        wk.fresh = !resident || uniform(ip->fresh);
+        wk.release = !resident || uniform(ip->release);
         rd.done(item_empty, lane);
         return true;
       };
-      // S of an item's first step: waits for its Q, and its K if new
-      auto first_s = [&](const Ring<NS> &rg) -> bool {
-        const uint32_t qs = X * QB + qc % QB;
-        const int st = rg.stage(resident, 0);
-        if (!warp_wait<32>(q_full + qs, (qc / QB) & 1, epoch, 3)) return false;
-        if (fresh && !warp_wait<32>(k_full + st, rg.phase(resident, 0), epoch, 4)) return false;
-        tc_fence_after();
-        if (leader) {
-          issue_s(qs, st);
-          // the stage is handed back at the last item that reads it
-          if (release) tc_commit(k_empty + st);
-          if (n == 1) tc_commit(q_empty + qs);
-        }
-        __syncwarp();
-        return true;
-      };
-      bool primed = false;                             // S of the item's first step is issued
       ok = fetch();
-      while (ok && n_qt > 0) {
-        const int cn = n;
-        const bool cfresh = fresh, crel = release, here = X < n_qt && n > 0;
-        if (here && !primed && !(ok = first_s(ring))) break;
-        primed = false;
-        const uint32_t qs = X * QB + qc % QB;
-        if (here) ++qc;
-        Ring<NS> next_ring = ring;                     // position of the next item
-        if (resident) next_ring.run += crel;
-        else next_ring.pos += cn;
+      while (ok && wk.n_qt > 0) {
+        const Work cur = wk;
+        const bool here = X < cur.n_qt && cur.n > 0;
         if (here) {
-          for (int j = 0; j < cn; ++j, ++steps) {
-            const bool more = j + 1 < cn;
-            const int st = ring.stage(resident, j), st1 = ring.stage(resident, j + 1);
-            if (cfresh) {
-              if (!(ok = warp_wait<32>(v_ready + st, ring.phase(resident, j), epoch, 5))) break;
-              if (more && !(ok = warp_wait<32>(k_full + st1, ring.phase(resident, j + 1), epoch, 4))) break;
-            }
-            if (!more && !(ok = fetch())) break;       // n, n_qt, fresh, release: now the next item's
-            if (!(ok = warp_wait<32>(p_full + X, steps & 1, epoch, 7))) break;
+          const uint32_t qs = X * QB + qc % QB;
+          const uint32_t qa = sdesc_lo<16>(aQ + qs * K::QTILE);
+          if (!(ok = mbar_wait(q_full + qs, (qc / QB) & 1, epoch))) break;
+          ++qc;
+          for (int j = 0; j < cur.n; ++j, ++steps) {
+            // S(j), over P(j - 1), which PV(j - 1) has read by then; only as many
+            // keys as there are (whole chunks)
+            const int sk = ring.stage<NSK>(resident, j), sv = ring.stage<NSV>(resident, j);
+            if (cur.fresh && !(ok = mbar_wait(k_full + sk, ring.phase<NSK>(resident, j), epoch))) break;
             tc_fence_after();
-            if (leader) {
-              const uint32_t va = aV + st * K::VTILE;
+            const int nk = cur.chunks(j);
+            const uint32_t ids = idesc_bf16(BLOCK_M, 0, 0, 0) | uint32_t(nk * 2) << 17;
+            const uint32_t ka = sdesc_lo<16>(aK + sk * K::KTILE);
 #pragma unroll
-              for (int kk = 0; kk < BN / 16; ++kk)
-                mma_ts(dO, dS + kk * 8, sdesc<K::VAT, 8 * K::VSW, layout_of(K::VSW)>(va + kk * 16 * K::VSW), IDPV,
-                       (j > 0 || kk > 0) ? 1u : 0u);
-              if (more) {
-                issue_s(qs, st1);                      // over P(j), which PV(j) has read by then
-                if (crel) {
-                  tc_commit(v_empty + st);
-                  tc_commit(k_empty + st1);
-                }
-                if (j + 2 == cn) tc_commit(q_empty + qs);
-              } else {
-                tc_commit(o_full + X);
-                if (crel) tc_commit(v_empty + st);
-              }
+            for (int kk = 0; kk < K::C0 / 16; ++kk)
+              mma_ss(lead, dS, sdesc<8 * K::SW0, layout_of(K::SW0)>(qa + kk * 2),
+                     sdesc<8 * K::SW0, layout_of(K::SW0)>(ka + kk * 2), ids, kk > 0);
+            if (K::C1) {
+#pragma unroll
+              for (int kk = 0; kk < K::C1X / 16; ++kk)
+                mma_ss(lead, dS, sdesc<8 * K::SW1X, layout_of(K::SW1X)>(qa + K::QT0 / 16 + kk * 2),
+                       sdesc<8 * K::SW1X, layout_of(K::SW1X)>(ka + K::KT0 / 16 + kk * 2), ids, 1);
             }
-            __syncwarp();
+            tc_commit(lead, s_full + X);
+            if (cur.release) tc_commit(lead, k_empty + sk);  // handed back at the last item that reads it
+            // PV(j)
+            if (cur.fresh && !(ok = mbar_wait(v_ready + sv, ring.phase<NSV>(resident, j), epoch))) break;
+            if (j + 1 == cur.n && !(ok = fetch())) break;    // wk: now the next item
+            const uint32_t va = sdesc_lo<K::VAT>(aV + sv * K::VTILE);
+            if (!(ok = mbar_wait(p_full + X, steps & 1, epoch))) break;
+            tc_fence_after();
+            constexpr uint32_t IDPV = idesc_bf16(BLOCK_M, K::DPV, 0, 1);
+#pragma unroll
+            for (int kk = 0; kk < K::CH; ++kk)
+              if (kk < nk)
+                mma_ts(lead, dO, dS + kk * 8, sdesc<8 * K::VSW, layout_of(K::VSW)>(va + kk * K::VSW), IDPV,
+                       (j > 0 || kk > 0) ? 1u : 0u);
+            if (j + 1 == cur.n) tc_commit(lead, o_full + X);
+            if (cur.release) tc_commit(lead, v_empty + sv);
           }
           if (!ok) break;
-          // straight on to the next item
-          if (X < n_qt && n > 0) {
-            if (!(ok = first_s(next_ring))) break;
-            primed = true;
-          }
         }
         // stages this tile did not use in this item: hand them back once they
         // were filled (a commit: earlier items of the run may still read them)
-        if (crel) {
-          const int last = resident ? a.max_steps : cn;
-          for (int j = here ? cn : 0; j < last && ok; ++j) {
-            const int st = ring.stage(resident, j);
-            const uint32_t ph = ring.phase(resident, j);
-            if (!(ok = warp_wait(k_full + st, ph, epoch, 8))) break;
-            if (!(ok = warp_wait(v_ready + st, ph, epoch, 9))) break;
-            if (leader) {
-              tc_commit(k_empty + st);
-              tc_commit(v_empty + st);
-            }
-            __syncwarp();
+        if (cur.release) {
+          const int last = resident ? a.max_steps : cur.n;
+          for (int j = here ? cur.n : 0; j < last && ok; ++j) {
+            const int sk = ring.stage<NSK>(resident, j), sv = ring.stage<NSV>(resident, j);
+            if (!(ok = mbar_wait(k_full + sk, ring.phase<NSK>(resident, j), epoch))) break;
+            tc_commit(lead, k_empty + sk);
+            if (!(ok = mbar_wait(v_ready + sv, ring.phase<NSV>(resident, j), epoch))) break;
+            tc_commit(lead, v_empty + sv);
           }
         }
+        if (resident) ring.run += cur.release;
+        else ring.pos += cur.n;
         if (!here && ok) ok = fetch();
-        ring = next_ring;
       }
+      if (!ok && lane == 0) gave_up(epoch, 1 + X);
       // every MMA issued completes before TMEM is released
       __syncwarp();
-      if (leader) {
-        tc_commit(mma_done + X);
-        mbar_drain(mma_done + X, 0);
-      }
-      __syncwarp();
-    } else if (warp == K::W_SCHED) {
-      // ================= scheduler =================
-      if (lane == 0) {
-        Walk<D> wk(a);
-        Item it;
-        if (wk.x < wk.end) it = decode<D>(a, sSet, wk.x);
-        else it.n_qt = 0;
-        it.fresh = 1;
-        for (uint32_t i = 0;; ++i) {
-          Item nx = it;
-          if (it.n_qt > 0) nx = wk.after(a, sSet, it);
-          it.release = it.n_qt > 0 && (nx.n_qt == 0 || nx.fresh);
-          if (!mbar_wait(item_empty + i % ITEMS, ((i / ITEMS) & 1) ^ 1, epoch, 16)) break;
-          sItem[i % ITEMS] = it;
-          mbar_arrive(item_full + i % ITEMS);
-          if (it.n_qt == 0) break;
-          it = nx;
-          wk.x += wk.inc;
-        }
-      }
+      tc_commit(lead, mma_done + X);
+      mbar_drain(mma_done + X, 0);
       __syncwarp();
     } else if (warp == K::W_FIX) {
       // ================= V rows of keys that do not count; ones column =================
       constexpr int A1 = K::ONES ? D / K::VW : 0, XB = (D % K::VW) * 2;
       bool ok = true;
-      Ring<NS> ring;
+      Ring ring;
       Reader rd;
       bool first = true;
       while (ok) {
-        const Item *ip = rd.get<0>(sItem, item_full, epoch, 15);
-        if (!ip) break;
+        const Item *ip = rd.get(sItem, item_full, epoch);
+        if (!(ok = ip != nullptr)) break;
         const Item it = *ip;
         rd.done(item_empty, lane);
         if (it.n_qt == 0) break;
@@ -851,28 +861,29 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         first = false;
         const int n = resident ? a.max_steps : it.n_kv;
         for (int j = 0; j < n; ++j) {
-          const int st = ring.stage(resident, j);
-          const uint32_t ph = ring.phase(resident, j);
+          const int st = ring.stage<NSV>(resident, j);
+          const uint32_t ph = ring.phase<NSV>(resident, j);
           const Step sp = step_of<BN>(it, j);
           const unsigned char *mk = a.c.seg[sp.seg].mask;
           const bool work = j < it.n_kv && (K::ONES || sp.valid < BN || mk);
-          bool keep[BN / 32];
+          bool keep[(BN + 31) / 32];
           if (work) {                          // before the wait: the mask bytes are on their way
             if (mk) mk += (long long)sp.set * a.c.seg[sp.seg].L + sp.key;
 #pragma unroll
-            for (int i = 0; i < BN / 32; ++i) {
+            for (int i = 0; i < (BN + 31) / 32; ++i) {
               const int r = lane + 32 * i;
               keep[i] = r < sp.valid && (!mk || st::after_wait(mk)[r]);
             }
           }
-          if (lane == 0) ok = mbar_wait(v_full + st, ph, epoch, 10);
+          if (lane == 0) ok = mbar_wait(v_full + st, ph, epoch);
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
           if (!ok) break;
           if (work) {
             uint8_t *vt = sV + st * K::VTILE;
 #pragma unroll
-            for (int i = 0; i < BN / 32; ++i) {
+            for (int i = 0; i < (BN + 31) / 32; ++i) {
               const int r = lane + 32 * i;
+              if (BN % 32 && r >= BN) continue;
               if (!keep[i]) {
                 for (int t = 0; t < K::VA; ++t)
 #pragma unroll
@@ -890,62 +901,78 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         }
         if (!resident) ring.pos += it.n_kv;
       }
+      if (!ok && lane == 0) gave_up(epoch, 1 + NT);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(K::R_SOFT));
-    // ================= softmax and epilogue of tile X =================
-    const int X = warp >> 2;                   // tile
+    // ================= softmax and epilogue of tile X, one thread per row =================
+    const int X = warp >> 2;
     const int r = ((warp & 3) << 5) + lane;    // row in tile == TMEM lane
     const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + X * K::TW;
     const uint32_t tO = tS + BN;
     const float sl2 = a.scale_log2;
-    const float2 scale2 = make_float2(sl2, sl2);
-    uint8_t *stg = sStg + warp * K::STG;
+    const f32x2 scale2 = pair(sl2, sl2);
     uint32_t gs = 0, oc = 0;                   // steps and items of this tile
+    bool pending = false;                      // O of the item before is on its way out of its Q slot
+    // Hands that slot to the loader once the store has read it.
+    auto release_slot = [&]() {
+      if (lane == 0 && pending) {
+        bulk_wait_read();
+        mbar_arrive(q_empty + X * QB + (oc - 1) % QB);
+      }
+      pending = false;
+    };
     bool ok = true;
     Reader rd;
     while (ok) {
-      const Item *ip = rd.get<8>(sItem, item_full, epoch, 15);
-      if (!ip) break;
-      const Item it = *ip;
-      rd.done(item_empty, lane);
+      const Item *ip = rd.get(sItem, item_full, epoch);
+      if (!(ok = ip != nullptr)) break;
+      const Item &it = *ip;                    // handed back at the end
+      const int n_kv = it.n_kv, n0 = it.n0, n1 = it.n1, s0 = it.s0, j0 = it.j0;
       if (it.n_qt == 0) break;
-      if (X >= it.n_qt) continue;
+      if (X >= it.n_qt) {
+        rd.done(item_empty, lane);
+        continue;
+      }
       float m = NO_KEY, l = 0.f;
-      for (int j = 0; j < it.n_kv; ++j, ++gs) {
-        const Step sp = step_of<BN>(it, j);
-        const unsigned char *mk = a.c.seg[sp.seg].mask;
-        uint32_t live[BN / 32];                // keys of the step that count, when some do not
-        const bool partial = sp.valid < BN || mk;
-        if (partial) {
-          if (mk) mk += (long long)sp.set * a.c.seg[sp.seg].L + sp.key;
+      for (int j = 0; j < n_kv; ++j, ++gs) {
+        const int g = j0 + j < s0 ? 0 : 1, key0 = (g ? j0 + j - s0 : j0 + j) * BN;
+        const int valid = (g ? n1 : n0) - key0;
+        const unsigned char *mk = a.c.seg[g].mask;
+        const bool part = valid < BN || mk;    // some of its keys do not count: `live` has a bit for each that does
+        uint32_t live[(BN + 31) / 32];
+        if (part) {
+          if (mk) mk += (long long)(g ? it.set1 : it.set0) * a.c.seg[g].L + key0;
 #pragma unroll
-          for (int i = 0; i < BN / 32; ++i)
-            live[i] = __ballot_sync(0xffffffffu, 32 * i + lane < sp.valid && (!mk || st::after_wait(mk)[32 * i + lane]));
+          for (int i = 0; i < (BN + 31) / 32; ++i)
+            live[i] = __ballot_sync(0xffffffffu, 32 * i + lane < valid && (!mk || st::after_wait(mk)[32 * i + lane]));
         }
-        if (!(ok = warp_wait<8>(s_full + X, gs & 1, epoch, 11))) break;
+        if (!(ok = mbar_wait(s_full + X, gs & 1, epoch))) break;
         tc_fence_after();
-        uint32_t sr[BN];
+        uint32_t sr[K::CH][16];
 #pragma unroll
-        for (int c = 0; c < BN / 16; ++c) COND_LD16(tS + c * 16, sr + c * 16);
+        for (int c = 0; c < K::CH; ++c) COND_LD16(tS + c * 16, sr[c]);   // (chunks past the keys hold anything)
         tmem_wait_ld();
-        if (partial) {
+        if (part) {
 #pragma unroll
-          for (int c = 0; c < BN; ++c)
-            if (!(live[c >> 5] >> (c & 31) & 1)) sr[c] = __float_as_uint(-INFINITY);
+          for (int c = 0; c < K::CH; ++c) {
+            const uint32_t keep = live[c >> 1] >> ((c & 1) * 16) & 0xffffu;
+            if (keep != 0xffffu) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (!(keep >> e & 1)) sr[c][e] = __float_as_uint(-INFINITY);
+            }
+          }
         }
         float mxp[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mxp[e] = __uint_as_float(sr[e]);
+        for (int e = 0; e < 4; ++e) mxp[e] = fmaxf(__uint_as_float(sr[0][2 * e]), __uint_as_float(sr[0][2 * e + 1]));
 #pragma unroll
-        for (int c = 4; c + 8 <= BN; c += 8) {
-          mxp[0] = fmax3(mxp[0], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-          mxp[1] = fmax3(mxp[1], __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
-          mxp[2] = fmax3(mxp[2], __uint_as_float(sr[c + 4]), __uint_as_float(sr[c + 5]));
-          mxp[3] = fmax3(mxp[3], __uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7]));
-        }
-        mxp[0] = fmax3(mxp[0], __uint_as_float(sr[BN - 4]), __uint_as_float(sr[BN - 3]));
-        mxp[1] = fmax3(mxp[1], __uint_as_float(sr[BN - 2]), __uint_as_float(sr[BN - 1]));
+        for (int c = 1; c < 2 * K::CH; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mxp[e] = fmax3(mxp[e], __uint_as_float(sr[c >> 1][(c & 1) * 8 + 2 * e]),
+                           __uint_as_float(sr[c >> 1][(c & 1) * 8 + 2 * e + 1]));
         // a step without any key leaves the row at NO_KEY: its weights are 0
         const float mx = fmaxf(fmaxf(fmax3(mxp[0], mxp[1], mxp[2]), mxp[3]) * sl2, NO_KEY);
         if (j == 0) {
@@ -960,148 +987,156 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
               m = mx;
             }
 #pragma unroll 1
-            for (int c = 0; c < K::DPV / 16; ++c) {
-              uint32_t ov[16];
-              COND_LD16(tO + c * 16, ov);
+            for (int c = 0; c < K::DPV / 8; ++c) {
+              uint32_t ov[8];
+              COND_LD8(tO + c * 8, ov);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
-              COND_ST16(tO + c * 16, ov);
+              for (int e = 0; e < 8; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
+              COND_ST8(tO + c * 8, ov);
             }
             tmem_wait_st();
           }
         }
-        const float2 negm = make_float2(-m, -m);
-        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const f32x2 negm = pair(-m, -m);
+        f32x2 acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
-        for (int c0 = 0; c0 < BN; c0 += 32) {
-          uint32_t pk[16];
+        for (int c = 0; c < K::CH; ++c) {
+          uint32_t pk[8];
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float2 xx = ffma2(make_float2(__uint_as_float(sr[c0 + c]), __uint_as_float(sr[c0 + c + 1])),
-                                    scale2, negm);
-            float2 e;
-            if (((c >> 1) & 7) < kPolyPairs) {
-              e = ex2_poly2(xx);
+          for (int e = 0; e < 8; ++e) {
+            const f32x2 xx = ffma2(pair(sr[c][2 * e], sr[c][2 * e + 1]), scale2, negm);
+            float2 w;
+            if (e < kPolyPairs) {
+              w = ex2_poly2(xx);
             } else {
-              e.x = ex2_mufu(xx.x);
-              e.y = ex2_mufu(xx.y);
+              w = unpair(xx);
+              w.x = ex2_mufu(w.x);
+              w.y = ex2_mufu(w.y);
             }
-            if (!K::ONES) acc[(c >> 1) & 3] = fadd2(acc[(c >> 1) & 3], e);
-            pk[c >> 1] = st::pack_bf16x2(e.x, e.y);
+            if (!K::ONES) acc[e & 1] = fadd2(acc[e & 1], pair(w.x, w.y));
+            pk[e] = st::pack_bf16x2(w.x, w.y);
           }
-          COND_ST16(tS + (c0 >> 1), pk);
+          COND_ST8(tS + c * 8, pk);
         }
         if (!K::ONES) {
-          const float2 s01 = fadd2(acc[0], acc[1]), s23 = fadd2(acc[2], acc[3]);
-          const float2 s = fadd2(s01, s23);
-          l += s.x + s.y;
+          const float2 t = unpair(fadd2(acc[0], acc[1]));
+          l += t.x + t.y;
         }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(p_full + X);
+        if (j == 0) release_slot();
       }
       if (!ok) break;
       // O of the item: divided by the row sum, written out.  P of the next item
       // follows in this warp, so its PV cannot overwrite O before it is read.
+      const bool some = n_kv > 0;
+      const bool tma = a.tma_out && some;      // (an item without keys has no slot)
       const int row = it.r0 + X * a.tile_rows + r;           // row of the unit
       const bool valid = r < a.tile_rows && row < a.c.R;
-      const bool some = it.n_kv > 0;
       float inv = 0.f, lse = -INFINITY;
+      uint8_t *stg = sQ + (X * QB + oc % QB) * K::QTILE;
       if (some) {
-        if (!(ok = warp_wait<8>(o_full + X, oc & 1, epoch, 13))) break;
+        if (!(ok = mbar_wait(o_full + X, oc & 1, epoch))) break;
         ++oc;
         tc_fence_after();
       }
-      const long long prow = (long long)it.split * a.c.part_rows + ((long long)it.unit * a.c.HW + it.w) * a.c.R + row;
-      const long long off = a.tma_out || !valid ? 0 : (a.c.part_o ? prow * D : st::cond_row(a.c, it.unit, it.w, row));
-      const int row0 = it.r0 + X * a.tile_rows + (warp & 3) * 32;
-      // O leaves TMEM from its last columns (which may hold the row sum), GRP
-      // chunks of 16 at a time
-      constexpr int NCH = (D + 15) / 16, GRP = D == 128 ? 4 : (D == 96 ? 3 : NCH);
+      // where the row goes without the tiled store
+      char *out = nullptr;
+      bool f32 = false;
+      if (!tma && valid) {
+        const long long prow = (long long)it.split * a.c.part_rows + ((long long)it.unit * a.c.HW + it.w) * a.c.R + row;
+        f32 = a.c.part_o || a.c.o_f32;
+        out = a.c.part_o ? reinterpret_cast<char *>(a.c.part_o + prow * D)
+                         : static_cast<char *>(a.c.o) + st::cond_row(a.c, it.unit, it.w, row) * (f32 ? 4 : 2);
+      }
+      // O leaves TMEM in groups of chunks of 16 columns, from the last ones
+      // (which may hold the row sum)
+      constexpr int NCH = (D + 15) / 16, GRP = NCH <= 5 ? NCH : NCH / 2;
+      if (some && K::ONES) {
+        uint32_t sum[8];                       // the sum of the bf16 weights
+        COND_LD8(tO + D, sum);
+        tmem_wait_ld();
+        l = __uint_as_float(sum[0]);
+      }
+      if (some && (m > NO_KEY || l != l)) {    // else no key counted: o = 0, lse = -inf
+        inv = __fdividef(1.0f, l);
+        lse = (m + __log2f(l)) * 0.6931471805599453f;
+      }
+      const f32x2 inv2 = pair(inv, inv);
+      if (tma) {
 #pragma unroll
-      for (int c0 = NCH; c0 > 0; c0 -= GRP) {
-        uint32_t ov[GRP][16];
+        for (int k0 = 0; k0 < NCH; k0 += GRP) {
+          uint32_t ov[GRP][16];
 #pragma unroll
-        for (int i = 0; i < GRP; ++i)
-          if (c0 - 1 - i >= 0) {
-            if (some) COND_LD16(tO + (c0 - 1 - i) * 16, ov[i]);
-            else
-#pragma unroll
-              for (int e = 0; e < 16; ++e) ov[i][e] = 0u;
-          }
-        if (some) {
+          for (int i = 0; i < GRP; ++i) COND_LD16(tO + (k0 + i) * 16, ov[i]);
           tmem_wait_ld();
-          if (c0 == NCH) {
-            if constexpr (K::ONES) l = __uint_as_float(ov[0][D % 16]);   // the sum of the bf16 weights
-            if (m > NO_KEY || l != l) {      // else no key counted: o = 0, lse = -inf
-              inv = __fdividef(1.0f, l);
-              lse = (m + __log2f(l)) * 0.6931471805599453f;
+          if (inv == 0.f) {                    // (O of such a row may hold anything)
+#pragma unroll
+            for (int i = 0; i < GRP; ++i)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ov[i][e] = 0;
+          }
+#pragma unroll
+          for (int i = 0; i < 2 * GRP; ++i) {  // 8 columns
+            const int f = 2 * k0 + i;
+            if (8 * f >= D) continue;
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int c = (i & 1) * 8 + 2 * e;
+              const float2 y = unpair(fmul2(pair(ov[i >> 1][c], ov[i >> 1][c + 1]), inv2));
+              v[e] = st::pack_bf16x2(y.x, y.y);
             }
+            uint8_t *dst;
+            if constexpr (K::DENSE) dst = stg + r * (2 * D) + 16 * f;
+            else if (8 * f < K::C0) dst = stg + r * K::SW0 + (swz<K::SW0>(r, f) << 4);
+            else dst = stg + K::QT0 + r * K::SW1X + (swz<K::SW1X>(r, f - K::C0 / 8) << 4);
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
-        if (a.tma_out) {
-          if (c0 == NCH) {
-            if (lane == 0) bulk_wait_read(); // the previous tile's store has read the staging rows
-            __syncwarp();
-          }
-          if (D == 128 && c0 == 4) {         // one 128-byte chunk of staging: the upper half goes out first
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (row0 < a.c.R) tma_store_5d(&mp.o1, stg, 64, it.w, row0, it.c3, it.c4);
-              bulk_commit();
-              bulk_wait_read();
-            }
-            __syncwarp();
-          }
-        }
+      } else {
+#pragma unroll 1
+        for (int f = 0; f < D / 8; ++f) {      // fp32 results, parts and packed heads: row by row
+          uint32_t ov[8];
+          COND_LD8(tO + 8 * f, ov);
+          tmem_wait_ld();
+          float y[8];
 #pragma unroll
-        for (int i = 0; i < GRP; ++i) {
-          const int c = (c0 - 1 - i) * 16;
-          if (c < 0) continue;
-          float y[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(ov[i][e]) * inv;
-          if (!a.tma_out && valid && (a.c.part_o || a.c.o_f32)) {
-            // a part without keys is not read by the combine kernel
-            float *dst = (a.c.part_o ? a.c.part_o : static_cast<float *>(a.c.o)) + off + c;
-#pragma unroll
-            for (int f = 0; f < 4; ++f)
-              if (c + 4 * f < D)
-                *reinterpret_cast<float4 *>(dst + 4 * f) = make_float4(y[4 * f], y[4 * f + 1], y[4 * f + 2], y[4 * f + 3]);
-          }
-          if (a.tma_out || (valid && !a.c.part_o && !a.c.o_f32)) {
-            // staged in the swizzle of the store's part of the head, or straight to the row
-            const bool lo = D == 128 || c < K::C0;
-            const int f0 = (c < K::C0 ? c : c - K::C0) / 8;
-            uint8_t *rowp = lo ? stg + lane * K::SW0 : stg + 32 * K::SW0 + lane * K::SW1X;
-            uint16_t *dst = static_cast<uint16_t *>(a.c.o) + off + c;
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              const int at = lo ? swz<K::SW0>(lane, f0 + f) : swz<K::SW1X>(lane, f0 + f);
-              const uint4 v = make_uint4(st::pack_bf16x2(y[8 * f], y[8 * f + 1]), st::pack_bf16x2(y[8 * f + 2], y[8 * f + 3]),
-                                         st::pack_bf16x2(y[8 * f + 4], y[8 * f + 5]), st::pack_bf16x2(y[8 * f + 6], y[8 * f + 7]));
-              if (a.tma_out) *reinterpret_cast<uint4 *>(rowp + (at << 4)) = v;
-              else if (c + 8 * f < D) *reinterpret_cast<uint4 *>(dst + 8 * f) = v;
-            }
+          for (int e = 0; e < 8; ++e) y[e] = inv == 0.f ? 0.f : __uint_as_float(ov[e]) * inv;
+          if (out && f32) {
+            *reinterpret_cast<float4 *>(out + 32 * f) = make_float4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<float4 *>(out + 32 * f + 16) = make_float4(y[4], y[5], y[6], y[7]);
+          } else if (out) {
+            *reinterpret_cast<uint4 *>(out + 16 * f) = make_uint4(st::pack_bf16x2(y[0], y[1]), st::pack_bf16x2(y[2], y[3]),
+                                                                  st::pack_bf16x2(y[4], y[5]), st::pack_bf16x2(y[6], y[7]));
           }
         }
       }
-      if (a.tma_out) {
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0 && row0 < a.c.R) {
-          tma_store_5d(&mp.o0, stg, 0, it.w, row0, it.c3, it.c4);
-          if (K::C1 && D != 128) tma_store_5d(&mp.o1, stg + 32 * K::SW0, 64, it.w, row0, it.c3, it.c4);
-          bulk_commit();
+      if (some) {
+        pending = true;
+        if (tma) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const int row0 = it.r0 + X * a.tile_rows + (warp & 3) * 32;
+            if (row0 < a.c.R) {
+              tma_store_5d(&mp.o0, stg + (warp & 3) * 32 * (K::DENSE ? 2 * D : K::SW0), 0, it.w, row0, it.c3, it.c4);
+              if (K::C1 && !K::DENSE) tma_store_5d(&mp.o1, stg + K::QT0 + (warp & 3) * 32 * K::SW1X, 64, it.w, row0, it.c3, it.c4);
+            }
+            bulk_commit();
+          }
         }
       }
       if (valid) {
-        if (a.c.part_o) a.c.part_lse[prow] = lse;
+        if (a.c.part_o)
+          a.c.part_lse[(long long)it.split * a.c.part_rows + ((long long)it.unit * a.c.HW + it.w) * a.c.R + row] = lse;
         else if (a.c.lse) a.c.lse[st::cond_lse(a.c, it.unit, it.w, row)] = lse;
       }
+      rd.done(item_empty, lane);
     }
+    if (!ok && lane == 0) gave_up(epoch, 8 + X);
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
@@ -1146,9 +1181,10 @@ bool encode(CUtensorMap *m, const void *ptr, int rank, const long long *dims, co
     if (i) s[i - 1] = (cuuint64_t)strides[i] * 2;
   }
   const CUtensorMapSwizzle sw = swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
-                                : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+                                : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                : swizzle_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_NONE;
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(ptr), d, s, b, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1194,6 +1230,8 @@ template <int D> st_status launch(const st::CondParams &p, cudaStream_t s) {
   a.dhw = st::make_fastdiv(uint32_t(p.HW));
   a.dkv = st::make_fastdiv(uint32_t(p.hdiv));
   a.dt = st::make_fastdiv(uint32_t(p.g.T));
+  a.dtblk = st::make_fastdiv(uint32_t(p.g.tblk));
+  a.n_tblk = p.g.T / p.g.tblk;
   long long steps = 0;
   Maps m;
   memset(&m, 0, sizeof(m));
@@ -1209,15 +1247,30 @@ template <int D> st_status launch(const st::CondParams &p, cudaStream_t s) {
   }
   if (steps * (p.n_split + 1) >= (1LL << 31)) return ST_ERR_SHAPE;
   a.max_steps = int(steps);
-  a.resident = p.n_split == 1 && steps <= K::NS ? 1 : 0;
+  a.resident = p.n_split == 1 && steps <= K::NSV ? 1 : 0;
   a.tma_out = !p.part_o && !p.o_f32 && p.G == 1 ? 1 : 0;
   if (!map_q(&m.q0, p.q, p, K::C0, K::SW0, a.tile_rows) ||
       (K::C1 && !map_q(&m.q1, p.q, p, K::C1X, K::SW1X, a.tile_rows)) ||
-      (a.tma_out && (!map_q(&m.o0, p.o, p, K::C0, K::SW0, 32) || (K::C1 && !map_q(&m.o1, p.o, p, K::C1X, K::SW1X, 32)))))
+      (a.tma_out && (!map_q(&m.o0, p.o, p, K::DENSE ? D : K::C0, K::DENSE ? 0 : K::SW0, 32) ||
+                     (K::C1 && !K::DENSE && !map_q(&m.o1, p.o, p, K::C1X, K::SW1X, 32)))))
     return ST_ERR_CUDA;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.epoch = g_epoch.fetch_add(1) + 1;
   const int ctas = int(items < st::num_sms() ? items : st::num_sms());
+  if (a.resident) {
+    // bands of one CTA each if that keeps the longest CTA as short as an even
+    // share of the items does, else bands of about that share, which a CTA may
+    // begin or end within
+    a.cols = st::cond_units(p) * p.HW;
+    const int share = (a.n_items + ctas - 1) / ctas;
+    const int whole = a.cols <= ctas ? (a.q_blocks + ctas / a.cols - 1) / (ctas / a.cols) : a.q_blocks + 1;
+    a.band = whole <= share ? whole : (share < a.q_blocks ? share : a.q_blocks);
+    a.n_bands = (a.q_blocks + a.band - 1) / a.band;
+    a.band_last = a.q_blocks - (a.n_bands - 1) * a.band;
+    a.dband = st::make_fastdiv(uint32_t(a.band));
+    a.dband_last = st::make_fastdiv(uint32_t(a.band_last));
+    a.dbandcols = st::make_fastdiv(uint32_t(a.band) * uint32_t(a.cols));
+  }
   auto kern = cond_attn_sm100<D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM) != cudaSuccess)
     return ST_ERR_CUDA;
@@ -1227,7 +1280,7 @@ template <int D> st_status launch(const st::CondParams &p, cudaStream_t s) {
   if (regs_ok < 0) {
     cudaFuncAttributes fa;
     if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return ST_ERR_CUDA;
-    regs_ok = fa.numRegs * K::THREADS >= 128 * K::NT * K::R_SOFT + 256 * K::R_MISC ? 1 : 0;
+    regs_ok = fa.numRegs * K::THREADS >= 128 * K::NT * K::R_SOFT + 32 * K::MISC * K::R_MISC ? 1 : 0;
   }
   if (!regs_ok) return ST_ERR_UNSUPPORTED;
   return st::launch_pdl(kern, dim3(ctas), dim3(K::THREADS), K::SMEM, s, m, a);
@@ -1249,7 +1302,9 @@ unsigned int read_and_clear_cond_error(cudaStream_t stream, cudaError_t *err) {
   return word;
 }
 
-CondTile cond_tile(int D) { return D <= 96 ? CondTile{3 * 128, 64} : CondTile{2 * 128, 128}; }
+CondTile cond_tile(int D) {
+  return D <= 96 ? CondTile{3 * 128, D <= 64 ? 96 : (D <= 80 ? 80 : 64)} : CondTile{2 * 128, 128};
+}
 
 st_status cond_sm100(const CondParams &p, cudaStream_t s) {
   switch (p.g.D) {
