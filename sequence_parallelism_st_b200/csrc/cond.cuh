@@ -55,6 +55,7 @@ struct CondParams {
   int n_seg;
   KvSeg own;                   // attended by the combine kernel (packed batches); own.k NULL: none
   int n_split;                 // parts the keys of a unit are split into
+  int spread;                  // parts that one work item takes side by side (1, or the tiles of an item)
   float scale;
   const void *q;
   void *o;
@@ -93,9 +94,9 @@ __device__ __forceinline__ long long cond_lse(const CondParams &p, int unit, int
 int device_sms();
 
 st_status cond_simt(const CondParams &p, st_dtype dtype, cudaStream_t s);
-// What the tensor-core kernel walks: rows per work item, keys per step.
+// What a kernel walks: rows of a tile, tiles of a work item, keys per step.
 struct CondTile {
-  int rows, keys;
+  int rows, tiles, keys;
 };
 CondTile cond_tile(int D);
 st_status cond_sm100(const CondParams &p, cudaStream_t s);

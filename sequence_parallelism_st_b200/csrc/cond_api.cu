@@ -146,48 +146,72 @@ st_status make_plan(const st_attn_desc *desc, const st_kv_desc *d0, const st_kv_
   p.scale = desc->scale > 0.f ? desc->scale : 1.0f / sqrtf((float)g.D);
   p.o_f32 = desc->o_fp32 || !bf16;
   pl.dtype = desc->dtype;
-  // split the keys when the items leave more than half of the GPU idle
-  const st::CondTile t = bf16 ? st::cond_tile(g.D) : st::CondTile{64, 64};
+  // split the keys when the items leave more than half of the GPU idle; items
+  // of one row tile then take one part of their keys with each of their tiles
+  const st::CondTile t = bf16 ? st::cond_tile(g.D) : st::CondTile{64, 1, 64};
   long long steps = 0;
   for (int i = 0; i < p.n_seg; ++i) steps += ceil_div(p.seg[i].L, t.keys);
-  const long long items = (long long)st::cond_units(p) * p.HW * ceil_div(p.R, t.rows);
+  const int tile_rows = bf16 ? t.rows / p.G * p.G : t.rows;
+  const long long items = (long long)st::cond_units(p) * p.HW * ceil_div(p.R, tile_rows * t.tiles);
   const long long cap = (long long)st::device_sms() * (bf16 ? 1 : 2);
-  p.n_split = 1;
+  p.n_split = p.spread = 1;
   const long long min_steps = ceil_div(MIN_KEYS, t.keys);
   if (with_ws && items * 2 <= cap && steps >= 2 * min_steps) {
+    if (p.R <= tile_rows) p.spread = t.tiles;
     long long n = cap / items;
     if (n > steps / min_steps) n = steps / min_steps;
-    p.n_split = int(n > MAX_SPLIT ? MAX_SPLIT : n);
+    if (n > MAX_SPLIT / p.spread) n = MAX_SPLIT / p.spread;
+    p.n_split = int(n) * p.spread;
   }
   pl.workspace = p.n_split > 1 || pack ? size_t(p.n_split) * size_t(p.part_rows) * size_t(g.D + 1) * 4 : 0;
   return ST_OK;
 }
 
 // ---------------------------------------------------------------- combine
-// One warp per row: the parts' weights exp(lse_c - M) (M the largest), the
-// weighted rows, and with OWN the row's own keys in the same softmax.  Parts
-// whose LSE is -inf (no key) are not read.  Bound by reading the partials.
-template <typename T, bool OWN>
+// The parts' weights exp(lse_c - M) (M the largest), the weighted rows, and
+// with OWN the row's own keys in the same softmax.  Parts whose LSE is -inf (no
+// key) are not read.  Bound by the latency of its chains of loads more than by
+// the bytes: WPR warps take a row (every WPR-th part and 32 keys), a lane holds
+// 4 consecutive channels, and the warps join over shared memory.
+__device__ __forceinline__ float4 load4(const uint16_t *p, int) {
+  const uint2 v = *reinterpret_cast<const uint2 *>(p);
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                     __uint_as_float(v.y & 0xffff0000u));
+}
+__device__ __forceinline__ float4 load4(const float *p, int n) {   // n: channels that exist; rows 4-byte aligned
+  return make_float4(p[0], n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
+}
+__device__ __forceinline__ void axpy4(float4 &a, float w, const float4 &x) {
+  a.x = fmaf(w, x.x, a.x);
+  a.y = fmaf(w, x.y, a.y);
+  a.z = fmaf(w, x.z, a.z);
+  a.w = fmaf(w, x.w, a.w);
+}
+
+template <typename T, bool OWN, int WPR>
 __global__ void __launch_bounds__(128) cond_combine(const __grid_constant__ CondParams p) {
-  __shared__ float sq[4][128];
+  __shared__ __align__(16) float sq[4][128];
+  __shared__ float sm[4], sl[4];
+  constexpr float L2E = 1.4426950408889634f;
   st::pdl_trigger();
   st::pdl_wait();
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-  const int D = p.g.D;
-  const long long row = (long long)blockIdx.x * 4 + wp;
-  if (row >= p.part_rows) return;
+  const int sub = wp % WPR;                    // this warp's share of the row
+  const int D = p.g.D, d0 = 4 * lane, nd = D - d0;
+  const long long row = (long long)blockIdx.x * (4 / WPR) + wp / WPR;
+  if (row >= p.part_rows) return;              // (WPR = 4: a block per row, none past the last)
   const int r = int(row % p.R);
   const int w = int(row / p.R % p.HW), unit = int(row / ((long long)p.R * p.HW));
   const long long off = st::cond_row(p, unit, w, r);
   const float *part_lse = st::after_wait(p.part_lse), *part_o = st::after_wait(p.part_o);
-  float m = -INFINITY, l = 0.f;                // own keys: running max (log2 units) and sum
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};         // channels lane + 32 i
+  float m = -INFINITY, l = 0.f;                // running max (log2 units) and sum; the same in all lanes
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if constexpr (OWN) {
     const T *q = static_cast<const T *>(st::after_wait(p.q)) + off;
-    const float sl2 = p.scale * 1.4426950408889634f;
-    for (int d = lane; d < D; d += 32) {
-      if constexpr (sizeof(T) == 2) sq[wp][d] = st::bf16_to_f32(q[d]) * sl2;
-      else sq[wp][d] = q[d] * sl2;
+    const float sl2 = p.scale * L2E;
+    if (nd > 0) {
+      const float4 x = load4(q + d0, nd);
+      *reinterpret_cast<float4 *>(&sq[wp][d0]) = make_float4(x.x * sl2, x.y * sl2, x.z * sl2, x.w * sl2);
     }
     __syncwarp();
     const int b = cond_batch(p, unit) + r / p.G / (p.T0 * p.S0);
@@ -200,13 +224,14 @@ __global__ void __launch_bounds__(128) cond_combine(const __grid_constant__ Cond
     const T *K = static_cast<const T *>(st::after_wait(sg.k)) + base;
     const T *V = static_cast<const T *>(st::after_wait(sg.v)) + base;
     const unsigned char *mk = sg.mask ? st::after_wait(sg.mask) + (long long)kr.set * sg.L : nullptr;
-    for (int k0 = 0; k0 < kr.n; k0 += 32) {
+    for (int k0 = 32 * sub; k0 < kr.n; k0 += 32 * WPR) {
       const int key = k0 + lane;
       float x = -INFINITY;
       if (key < kr.n && (!mk || mk[key])) {    // one key per lane
         const T *kp = K + (long long)key * sg.stride_l;
         x = 0.f;
         if constexpr (sizeof(T) == 2) {
+#pragma unroll 4
           for (int d = 0; d < D; d += 8) {
             const uint4 v = *reinterpret_cast<const uint4 *>(kp + d);
             const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -217,6 +242,7 @@ __global__ void __launch_bounds__(128) cond_combine(const __grid_constant__ Cond
             }
           }
         } else {
+#pragma unroll 8
           for (int d = 0; d < D; ++d) x = fmaf(sq[wp][d], kp[d], x);
         }
       }
@@ -231,29 +257,21 @@ __global__ void __launch_bounds__(128) cond_combine(const __grid_constant__ Cond
       for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
       l = l * corr + sum;
       m = mn;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] *= corr;
-      const unsigned live = __ballot_sync(0xffffffffu, e != 0.f);
+      acc = make_float4(acc.x * corr, acc.y * corr, acc.z * corr, acc.w * corr);
+      const unsigned counts = __ballot_sync(0xffffffffu, e != 0.f);
       const int nk = min(32, kr.n - k0);
-      for (int k = 0; k < nk; ++k) {
-        if (!(live >> k & 1)) continue;        // a key that does not count is not read
+#pragma unroll 8
+      for (int k = 0; k < nk; ++k) {           // a key that does not count is not read
         const float pk = __shfl_sync(0xffffffffu, e, k);
-        const T *vp = V + (long long)(k0 + k) * sg.stride_l;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int d = lane + 32 * i;
-          if (d < D) {
-            if constexpr (sizeof(T) == 2) acc[i] = fmaf(pk, st::bf16_to_f32(vp[d]), acc[i]);
-            else acc[i] = fmaf(pk, vp[d], acc[i]);
-          }
-        }
+        if ((counts >> k & 1) && nd > 0) axpy4(acc, pk, load4(V + (long long)(k0 + k) * sg.stride_l + d0, nd));
       }
     }
   }
-  const float L2E = 1.4426950408889634f;
+  // the parts: sub, sub + WPR, ... (at most 64 in all)
   const int n = p.n_split;
-  const float l0 = lane < n ? part_lse[(long long)lane * p.part_rows + row] : -INFINITY;
-  const float l1 = lane + 32 < n ? part_lse[(long long)(lane + 32) * p.part_rows + row] : -INFINITY;
+  const int c0 = sub + WPR * lane, c1 = c0 + 32 * WPR;
+  const float l0 = c0 < n ? part_lse[(long long)c0 * p.part_rows + row] : -INFINITY;
+  const float l1 = c1 < n ? part_lse[(long long)c1 * p.part_rows + row] : -INFINITY;
   float M = fmaxf(l0, l1) * L2E;
 #pragma unroll
   for (int y = 16; y > 0; y >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, y));
@@ -265,31 +283,60 @@ __global__ void __launch_bounds__(128) cond_combine(const __grid_constant__ Cond
 #pragma unroll
   for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
   sum += l * own;
+  acc = make_float4(acc.x * own, acc.y * own, acc.z * own, acc.w * own);
+#pragma unroll 4
+  for (int i = 0; sub + WPR * i < n; ++i) {
+    const float wc = __shfl_sync(0xffffffffu, i < 32 ? w0 : w1, i & 31);
+    if (wc != 0.f && nd > 0) {
+      const float *src = part_o + ((long long)(sub + WPR * i) * p.part_rows + row) * D + d0;
+      if constexpr (sizeof(T) == 2) axpy4(acc, wc, *reinterpret_cast<const float4 *>(src));
+      else axpy4(acc, wc, load4(src, nd));
+    }
+  }
+  if constexpr (WPR > 1) {                     // join the warps of the row
+    if (lane == 0) {
+      sm[wp] = M;
+      sl[wp] = sum;
+    }
+    __syncthreads();
+    const float all = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+    const float base = all == -INFINITY ? 0.f : all;
+    const float scale = exp2f(M - base);       // 0 for a warp without a key
+    *reinterpret_cast<float4 *>(&sq[wp][d0]) = make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
+    sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] *= own;
-  for (int c = 0; c < n; ++c) {
-    const float wc = __shfl_sync(0xffffffffu, c < 32 ? w0 : w1, c & 31);
-    if (wc == 0.f) continue;
-    const float *src = part_o + ((long long)c * p.part_rows + row) * D;
+    for (int i = 0; i < 4; ++i) sum = fmaf(sl[i], exp2f(sm[i] - base), sum);
+    M = all;
+    __syncthreads();
+    if (sub) return;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 32 * i < D) acc[i] = fmaf(wc, src[lane + 32 * i], acc[i]);
+    for (int i = 0; i < 4; ++i) axpy4(acc, 1.f, *reinterpret_cast<const float4 *>(&sq[i][d0]));
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+  if (nd > 0) {
+    if (p.o_f32) {
+      float *o = static_cast<float *>(p.o) + off + d0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int d = lane + 32 * i;
-    if (d >= D) continue;
-    if (p.o_f32) static_cast<float *>(p.o)[off + d] = acc[i] * inv;
-    else static_cast<uint16_t *>(p.o)[off + d] = st::f32_to_bf16(acc[i] * inv);
+      for (int i = 0; i < 4; ++i)
+        if (i < nd) o[i] = y[i];
+    } else {
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + off + d0) =
+          make_uint2(st::pack_bf16x2(y[0], y[1]), st::pack_bf16x2(y[2], y[3]));
+    }
   }
-  if (p.lse && lane == 0) p.lse[st::cond_lse(p, unit, w, r)] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) / L2E;
+  if (p.lse && lane == 0) p.lse[st::cond_lse(p, unit, w, r)] = sum == 0.f ? -INFINITY : (M + log2f(sum)) / L2E;
 }
 
+// Four warps per row while that many blocks still run at once; else a warp.
+template <typename T, bool OWN> st_status combine_own(const CondParams &p, cudaStream_t s) {
+  if (p.part_rows <= (long long)st::device_sms() * 16)
+    return st::launch_pdl(cond_combine<T, OWN, 4>, dim3(unsigned(p.part_rows)), dim3(128), 0, s, p);
+  return st::launch_pdl(cond_combine<T, OWN, 1>, dim3(unsigned((p.part_rows + 3) / 4)), dim3(128), 0, s, p);
+}
 template <typename T> st_status combine(const CondParams &p, cudaStream_t s) {
-  const long long grid = (p.part_rows + 3) / 4;
-  if (p.own.k) return st::launch_pdl(cond_combine<T, true>, dim3(unsigned(grid)), dim3(128), 0, s, p);
-  return st::launch_pdl(cond_combine<T, false>, dim3(unsigned(grid)), dim3(128), 0, s, p);
+  return p.own.k ? combine_own<T, true>(p, s) : combine_own<T, false>(p, s);
 }
 
 st_status run(const st_attn_desc *desc, const st_kv_desc *d0, const st_kv_desc *d1, const void *q, const void *k0,

@@ -80,22 +80,31 @@ template <int D> struct Cfg {
   static constexpr bool ONES = DPV > D;
   static constexpr int TW = BN + DPV;                  // TMEM columns of a tile: S (P over it), O
   static_assert(NT * TW <= 512, "TMEM");
-  // Two Q tiles per row tile, its own so that its issuer sees every phase.  An
-  // item's O is staged over its Q (dead by then) and stored from there, while
-  // the next item's Q is already in the other: rows of 144 and 160 bytes as they
-  // are (16-byte stores of 8 lanes then meet at most 2 to a bank), the other
-  // widths in the layout of Q.
-  static constexpr int QB = 2, NQ = NT * QB;
+  // Q tiles: two items' worth, used in turn.  An item's O is staged over its Q
+  // (dead by then) and stored from there, while the next item's Q is already in
+  // the others: rows of 144 and 160 bytes as they are (16-byte stores of 8
+  // lanes then meet at most 2 to a bank), the other widths in the layout of Q.
+  // At head dim 128 one of the four gives way to a fourth K/V tile where the
+  // keys take more than one step (TIGHT): row tile 1 then runs a step behind
+  // row tile 0, in whose place its next Q goes.  (2 K and 1 V: 955 TF/s over
+  // 4096 keys.  K and V in turn in three tiles: 874.)
+  static constexpr int NQ = 2 * NT;
+  static constexpr bool TIGHT = D == 128;
   static constexpr bool DENSE = D == 72 || D == 80;
   static_assert(!DENSE || BLOCK_M * 2 * D <= QTILE, "O over Q");
   static constexpr int TABLE = D == 128 ? 32 : 64;     // key ranges of a segment held in shared memory
   static constexpr int TAIL = 2 * TABLE * 8 + 512 + (D == 128 ? 512 : 768);    // key ranges, items, barriers
   static constexpr int ROOM = 232448 - 1024 - TAIL - NQ * QTILE;
   // K and V stages: as many of both as fit, at most 8; an odd K tile more
-  static constexpr int NSV = ROOM / (KTILE + VTILE) > 8 ? 8 : ROOM / (KTILE + VTILE);
-  static constexpr int NSK = NSV < 8 && ROOM - NSV * (KTILE + VTILE) >= KTILE ? NSV + 1 : NSV;
-  static constexpr int SMEM = 1024 + NQ * QTILE + NSK * KTILE + NSV * VTILE + TAIL;
-  static_assert(SMEM <= 232448 && NSV >= 1 && NSK >= 2, "shared memory");
+  static constexpr int NSV = TIGHT ? 2 : (ROOM / (KTILE + VTILE) > 8 ? 8 : ROOM / (KTILE + VTILE));
+  static constexpr int NSK = !TIGHT && NSV < 8 && ROOM - NSV * (KTILE + VTILE) >= KTILE ? NSV + 1 : NSV;
+  // streaming uses a multiple of NT: with the keys of an item spread over the
+  // tiles, a stage then belongs to one tile
+  static constexpr int SSK = NSK / NT * NT, SSV = NSV / NT * NT;
+  static constexpr int KV_BYTES = NSK * KTILE + NSV * VTILE;
+  static constexpr int SMEM = 1024 + (NQ - TIGHT) * QTILE + KV_BYTES + TAIL;
+  static_assert(SMEM <= 232448 && SSK >= NT && SSV >= NT, "shared memory");
+  static_assert(!TIGHT || (KTILE == QTILE && VTILE == QTILE), "a Q tile gives way to a K/V tile");
   // warps: softmax and epilogue of the tiles, then loader, issuers, V helper;
   // the rest of the last two warpgroups idles
   static constexpr int W_LOAD = 4 * NT, W_MMA = W_LOAD + 1, W_FIX = W_MMA + NT;
@@ -368,6 +377,9 @@ struct Args {
   int n_items;
   int resident;                // every key tile of an item fits the ring: K and V stay from item to item
   int max_steps;
+  int spread;                  // the tiles of a CTA take the same rows and every NT-th step
+  int nq;                      // TIGHT: Q slots
+  int n_split;                 // parts of an item's keys (each NT of the call's parts with spread)
   int tma_out;                 // bf16 rows go out as tiles
   float scale_log2;
   uint32_t epoch;
@@ -411,7 +423,7 @@ template <int BN> __device__ __forceinline__ Step step_of(const Item &it, int j)
 template <int D> __device__ __forceinline__ void rows_of(const Args &a, Item &it) {
   it.r0 = it.qb * Cfg<D>::NT * a.tile_rows;
   const int left = a.c.R - it.r0;
-  it.n_qt = left > 2 * a.tile_rows && Cfg<D>::NT > 2 ? 3 : (left > a.tile_rows ? 2 : 1);
+  it.n_qt = a.spread ? Cfg<D>::NT : left > 2 * a.tile_rows && Cfg<D>::NT > 2 ? 3 : (left > a.tile_rows ? 2 : 1);
 }
 
 // Streaming: q block fastest, then split, head, unit.  Resident: q block of a
@@ -435,7 +447,7 @@ __device__ __forceinline__ Item decode(const Args &a, const int2 *table, int x) 
     it.qb = x - int(y) * a.q_blocks;
     it.qb_end = a.q_blocks;
     z = st::fdiv(y, a.dsplit);
-    it.split = int(y) - int(z) * a.c.n_split;
+    it.split = int(y) - int(z) * a.n_split;
   }
   it.unit = int(st::fdiv(z, a.dhw));
   it.w = int(z) - it.unit * a.c.HW;
@@ -469,7 +481,7 @@ __device__ __forceinline__ Item decode(const Args &a, const int2 *table, int x) 
   range(1, it.set1, it.row1, it.n1);
   it.s0 = (it.n0 + K::BN - 1) / K::BN;
   const int total = it.s0 + (it.n1 + K::BN - 1) / K::BN;
-  if (a.c.n_split == 1) {
+  if (a.n_split == 1) {
     it.j0 = 0;
     it.n_kv = total;
   } else {
@@ -539,21 +551,39 @@ struct Ring {
   }
 };
 
+// The steps of an item a tile takes: all, or (keys spread over the tiles) every
+// NT-th, by the position in the ring: step j of an item that began at `pos`
+// belongs to tile (pos + j) % NT.
+template <int NT> __device__ __forceinline__ int first_step(bool spread, uint32_t pos, int X) {
+  if (!spread) return 0;
+  const int f = X - int(pos % NT);
+  return f < 0 ? f + NT : f;
+}
+// Its place among the item's Q tiles.
+__device__ __forceinline__ int q_index(bool spread, int first, int X) { return spread ? first : X; }
+// Q tiles of an item: of every tile that has a step of it.
+__device__ __forceinline__ int q_tiles(bool spread, int n_qt, int n_kv) {
+  return spread ? min(n_qt, n_kv) : (n_kv > 0 ? n_qt : 0);
+}
+// Slot `i` of the Q tiles after slot q0.
+__device__ __forceinline__ int q_slot(int q0, int i, int nq) { return q0 + i >= nq ? q0 + i - nq : q0 + i; }
+
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     cond_attn_sm100(const __grid_constant__ Maps mp, const __grid_constant__ Args a) {
   using K = Cfg<D>;
-  constexpr int NT = K::NT, NSK = K::NSK, NSV = K::NSV, NQ = K::NQ, QB = K::QB, BN = K::BN;
+  constexpr int NT = K::NT, NSK = K::NSK, NSV = K::NSV, NQ = K::NQ, BN = K::BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sQ = base;
-  uint8_t *sK = sQ + NQ * K::QTILE;
-  uint8_t *sV = sK + NSK * K::KTILE;
-  int2 *sSet = reinterpret_cast<int2 *>(sV + NSV * K::VTILE);
+  const int nq = K::TIGHT ? a.nq : NQ;       // Q slots; K tiles behind them, then V tiles
+  uint8_t *sK = sQ + nq * K::QTILE;
+  uint8_t *sV = sK + (K::TIGHT ? NQ + 1 - nq : NSK) * K::KTILE;
+  int2 *sSet = reinterpret_cast<int2 *>(sQ + (NQ - K::TIGHT) * K::QTILE + K::KV_BYTES);
   Item *sItem = reinterpret_cast<Item *>(sSet + 2 * K::TABLE);
   uint64_t *bars = reinterpret_cast<uint64_t *>(sItem + ITEMS);
-  uint64_t *q_full = bars, *q_empty = q_full + NQ;
-  uint64_t *k_full = q_empty + NQ, *k_empty = k_full + NSK;      // k_empty, v_empty: one arrival per tile
+  uint64_t *q_full = bars, *q_empty = q_full + NQ;   // q_full: two per tile, its Q tiles in turn; q_empty: by slot
+  uint64_t *k_full = q_empty + NQ, *k_empty = k_full + NSK;      // k_empty, v_empty: one arrival per tile that reads the stage
   uint64_t *v_full = k_empty + NSK, *v_empty = v_full + NSV, *v_ready = v_empty + NSV;
   // per tile: S ready; P written; O of an item complete
   uint64_t *s_full = v_ready + NSV, *p_full = s_full + NT, *o_full = p_full + NT;
@@ -569,11 +599,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     }
     for (int i = 0; i < NSK; ++i) {
       mbar_init(k_full + i, 1);
-      mbar_init(k_empty + i, NT);
+      mbar_init(k_empty + i, a.spread ? 1 : NT);
     }
     for (int i = 0; i < NSV; ++i) {
       mbar_init(v_full + i, 1);
-      mbar_init(v_empty + i, NT);
+      mbar_init(v_empty + i, a.spread ? 1 : NT);
       mbar_init(v_ready + i, 1);
     }
     for (int i = 0; i < NT; ++i) {
@@ -612,7 +642,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t epoch = a.epoch;
-  const bool resident = a.resident != 0;
+  const bool resident = a.resident != 0, spread = a.spread != 0;
 
   if (warp >= K::W_LOAD) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K::R_MISC));
@@ -622,11 +652,42 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       if (lane == 0) {
         bool ok = true;
         Ring ring;
-        uint32_t qn = 0;                              // 2 bits per tile: its Q tiles so far (slot, phase)
+        uint32_t qn = 0;                              // 2 bits per tile: its Q tiles so far (barrier, phase)
         int last_kv = -1;                             // streaming: ring position of the last K/V issued
         int loaded = 0;                               // resident: stages loaded in this run
         bool first = true;
         Walk wk(a);
+        const bool tight = K::TIGHT && nq < NQ;
+        int q0 = 0;                                   // next Q slot
+        uint32_t q_phase = 1;                         // parity its release shows
+        // the item's Q tiles [i0, i1)
+        auto load_q = [&](const Item &it, int i0, int i1) -> bool {
+          i1 = min(i1, q_tiles(spread, it.n_qt, it.n_kv));
+#pragma unroll 1
+          for (int i = i0; i < i1; ++i) {
+            const int X = spread ? int((ring.pos + i) % NT) : i;
+            const uint32_t n = qn >> 2 * X & 3;
+            uint64_t *full = q_full + 2 * X + (n & 1);
+            const int slot = K::TIGHT ? q0 : 2 * X + int(n & 1);
+            if (!(ok = mbar_wait(q_empty + slot, K::TIGHT ? q_phase : (n >> 1) ^ 1, epoch))) return false;
+            qn ^= (n ^ ((n + 1) & 3)) << 2 * X;
+            uint8_t *dst = sQ + slot * K::QTILE;
+            if (K::TIGHT && ++q0 == nq) {
+              q0 = 0;
+              q_phase ^= 1;
+            }
+            const int row = it.r0 + (spread ? 0 : X * a.tile_rows);
+            mbar_expect_tx(full, a.tile_rows * (K::SW0 + K::SW1));
+            if (a.c.G > 1) {
+              tma_load_5d(dst, &mp.q0, full, 0, 0, it.w, row / a.c.G, it.unit);
+              if (K::C1) tma_load_5d(dst + K::QT0, &mp.q1, full, 64, 0, it.w, row / a.c.G, it.unit);
+            } else {
+              tma_load_5d(dst, &mp.q0, full, 0, it.w, row, it.c3, it.c4);
+              if (K::C1) tma_load_5d(dst + K::QT0, &mp.q1, full, 64, it.w, row, it.c3, it.c4);
+            }
+          }
+          return true;
+        };
         Item sch;                                     // the item to publish
         sch.n_qt = 1;
         sch.qb = sch.qb_end = 0;
@@ -662,13 +723,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           first = false;
           const int n = resident ? (load_kv ? a.max_steps : 1) : it.n_kv;
           for (int j = 0; j < n && ok; ++j) {
-            const int sk = ring.stage<NSK>(resident, j), sv = ring.stage<NSV>(resident, j);
+            const int sk = ring.stage<K::SSK>(resident, j), sv = ring.stage<K::SSV>(resident, j);
             const Step sp = step_of<BN>(it, j);
             const int g = sp.seg;
             const int set = a.c.seg[g].offsets ? 0 : sp.set;   // packed: rows of one long sequence
             const bool real = j < it.n_kv;            // resident: stages past the item's steps only change phase
             if (load_kv) {
-              if (!(ok = mbar_wait(k_empty + sk, ring.phase<NSK>(resident, j) ^ 1, epoch))) break;
+              if (!(ok = mbar_wait(k_empty + sk, ring.phase<K::SSK>(resident, j) ^ 1, epoch))) break;
               if (real) {
                 mbar_expect_tx(k_full + sk, K::KBYTES);
                 uint8_t *dk = sK + sk * K::KTILE;
@@ -680,28 +741,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 mbar_arrive(k_full + sk);
               }
             }
-            if (j == 0 && it.n_kv > 0) {
-#pragma unroll 1
-              for (int X = 0; X < it.n_qt; ++X) {
-                const uint32_t n = qn >> 2 * X & 3;
-                const int qs = X * QB + (n & 1);
-                if (!(ok = mbar_wait(q_empty + qs, (n >> 1) ^ 1, epoch))) break;
-                qn ^= (n ^ ((n + 1) & 3)) << 2 * X;
-                uint8_t *dst = sQ + qs * K::QTILE;
-                const int row = it.r0 + X * a.tile_rows;
-                mbar_expect_tx(q_full + qs, a.tile_rows * (K::SW0 + K::SW1));
-                if (a.c.G > 1) {
-                  tma_load_5d(dst, &mp.q0, q_full + qs, 0, 0, it.w, row / a.c.G, it.unit);
-                  if (K::C1) tma_load_5d(dst + K::QT0, &mp.q1, q_full + qs, 64, 0, it.w, row / a.c.G, it.unit);
-                } else {
-                  tma_load_5d(dst, &mp.q0, q_full + qs, 0, it.w, row, it.c3, it.c4);
-                  if (K::C1) tma_load_5d(dst + K::QT0, &mp.q1, q_full + qs, 64, it.w, row, it.c3, it.c4);
-                }
-              }
-              if (!ok) break;
-            }
+            if (j == 0 && !load_q(it, 0, tight ? 1 : NT)) break;
             if (load_kv) {
-              if (!(ok = mbar_wait(v_empty + sv, ring.phase<NSV>(resident, j) ^ 1, epoch))) break;
+              if (!(ok = mbar_wait(v_empty + sv, ring.phase<K::SSV>(resident, j) ^ 1, epoch))) break;
               if (real) {
                 mbar_expect_tx(v_full + sv, K::VTILE);
                 uint8_t *dv = sV + sv * K::VTILE;
@@ -712,6 +754,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 mbar_arrive(v_full + sv);
               }
             }
+            if (tight && j == (n > 1 ? 1 : 0) && !load_q(it, 1, NT)) break;
           }
           if (!resident) ring.pos += it.n_kv;
         }
@@ -725,13 +768,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
               mbar_drain(v_full + j, ring.run & 1);
             }
           } else {
-            for (int i = last_kv; i >= 0 && i > last_kv - NSK; --i) mbar_drain(k_full + i % NSK, (i / NSK) & 1);
-            for (int i = last_kv; i >= 0 && i > last_kv - NSV; --i) mbar_drain(v_full + i % NSV, (i / NSV) & 1);
+            for (int i = last_kv; i >= 0 && i > last_kv - K::SSK; --i) mbar_drain(k_full + i % K::SSK, (i / K::SSK) & 1);
+            for (int i = last_kv; i >= 0 && i > last_kv - K::SSV; --i) mbar_drain(v_full + i % K::SSV, (i / K::SSV) & 1);
           }
           for (int X = 0; X < NT; ++X)
-            for (uint32_t k = 1; k <= 2; ++k) {       // (a slot never loaded answers at once)
+            for (uint32_t k = 1; k <= 2; ++k) {       // (a barrier never used answers at once)
               const uint32_t n = ((qn >> 2 * X) - k) & 3;
-              mbar_drain(q_full + X * QB + (n & 1), n >> 1);
+              mbar_drain(q_full + 2 * X + (n & 1), n >> 1);
             }
         }
       }
@@ -749,6 +792,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       Ring ring;
       Reader rd;
       uint32_t qc = 0, steps = 0;                      // Q tiles and steps of this tile so far
+      int q0 = 0;                                      // first Q slot of the item
       struct Work {                                    // what the issuer needs of an item
         int n_qt, n, n0, n1, s0, j0;
         bool fresh, release;
@@ -777,17 +821,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       ok = fetch();
       while (ok && wk.n_qt > 0) {
         const Work cur = wk;
-        const bool here = X < cur.n_qt && cur.n > 0;
+        const int j0 = first_step<NT>(spread, ring.pos, X), inc = spread ? NT : 1;
+        const bool here = X < cur.n_qt && j0 < cur.n;
         if (here) {
-          const uint32_t qs = X * QB + qc % QB;
-          const uint32_t qa = sdesc_lo<16>(aQ + qs * K::QTILE);
-          if (!(ok = mbar_wait(q_full + qs, (qc / QB) & 1, epoch))) break;
+          const int slot = K::TIGHT ? q_slot(q0, q_index(spread, j0, X), nq) : 2 * X + int(qc & 1);
+          const uint32_t qa = sdesc_lo<16>(aQ + slot * K::QTILE);
+          if (!(ok = mbar_wait(q_full + 2 * X + (qc & 1), (qc >> 1) & 1, epoch))) break;
           ++qc;
-          for (int j = 0; j < cur.n; ++j, ++steps) {
+          for (int j = j0; j < cur.n; j += inc, ++steps) {
             // S(j), over P(j - 1), which PV(j - 1) has read by then; only as many
             // keys as there are (whole chunks)
-            const int sk = ring.stage<NSK>(resident, j), sv = ring.stage<NSV>(resident, j);
-            if (cur.fresh && !(ok = mbar_wait(k_full + sk, ring.phase<NSK>(resident, j), epoch))) break;
+            const int sk = ring.stage<K::SSK>(resident, j), sv = ring.stage<K::SSV>(resident, j);
+            if (cur.fresh && !(ok = mbar_wait(k_full + sk, ring.phase<K::SSK>(resident, j), epoch))) break;
             tc_fence_after();
             const int nk = cur.chunks(j);
             const uint32_t ids = idesc_bf16(BLOCK_M, 0, 0, 0) | uint32_t(nk * 2) << 17;
@@ -805,8 +850,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             tc_commit(lead, s_full + X);
             if (cur.release) tc_commit(lead, k_empty + sk);  // handed back at the last item that reads it
             // PV(j)
-            if (cur.fresh && !(ok = mbar_wait(v_ready + sv, ring.phase<NSV>(resident, j), epoch))) break;
-            if (j + 1 == cur.n && !(ok = fetch())) break;    // wk: now the next item
+            if (cur.fresh && !(ok = mbar_wait(v_ready + sv, ring.phase<K::SSV>(resident, j), epoch))) break;
+            const bool last = j + inc >= cur.n;
+            if (last && !(ok = fetch())) break;              // wk: now the next item
             const uint32_t va = sdesc_lo<K::VAT>(aV + sv * K::VTILE);
             if (!(ok = mbar_wait(p_full + X, steps & 1, epoch))) break;
             tc_fence_after();
@@ -815,24 +861,25 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             for (int kk = 0; kk < K::CH; ++kk)
               if (kk < nk)
                 mma_ts(lead, dO, dS + kk * 8, sdesc<8 * K::VSW, layout_of(K::VSW)>(va + kk * K::VSW), IDPV,
-                       (j > 0 || kk > 0) ? 1u : 0u);
-            if (j + 1 == cur.n) tc_commit(lead, o_full + X);
+                       (j > j0 || kk > 0) ? 1u : 0u);
+            if (last) tc_commit(lead, o_full + X);
             if (cur.release) tc_commit(lead, v_empty + sv);
           }
           if (!ok) break;
         }
         // stages this tile did not use in this item: hand them back once they
         // were filled (a commit: earlier items of the run may still read them)
-        if (cur.release) {
+        if (cur.release && !spread) {
           const int last = resident ? a.max_steps : cur.n;
           for (int j = here ? cur.n : 0; j < last && ok; ++j) {
-            const int sk = ring.stage<NSK>(resident, j), sv = ring.stage<NSV>(resident, j);
-            if (!(ok = mbar_wait(k_full + sk, ring.phase<NSK>(resident, j), epoch))) break;
+            const int sk = ring.stage<K::SSK>(resident, j), sv = ring.stage<K::SSV>(resident, j);
+            if (!(ok = mbar_wait(k_full + sk, ring.phase<K::SSK>(resident, j), epoch))) break;
             tc_commit(lead, k_empty + sk);
-            if (!(ok = mbar_wait(v_ready + sv, ring.phase<NSV>(resident, j), epoch))) break;
+            if (!(ok = mbar_wait(v_ready + sv, ring.phase<K::SSV>(resident, j), epoch))) break;
             tc_commit(lead, v_empty + sv);
           }
         }
+        if (K::TIGHT) q0 = q_slot(q0, q_tiles(spread, cur.n_qt, cur.n), nq);
         if (resident) ring.run += cur.release;
         else ring.pos += cur.n;
         if (!here && ok) ok = fetch();
@@ -861,8 +908,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         first = false;
         const int n = resident ? a.max_steps : it.n_kv;
         for (int j = 0; j < n; ++j) {
-          const int st = ring.stage<NSV>(resident, j);
-          const uint32_t ph = ring.phase<NSV>(resident, j);
+          const int st = ring.stage<K::SSV>(resident, j);
+          const uint32_t ph = ring.phase<K::SSV>(resident, j);
           const Step sp = step_of<BN>(it, j);
           const unsigned char *mk = a.c.seg[sp.seg].mask;
           const bool work = j < it.n_kv && (K::ONES || sp.valid < BN || mk);
@@ -912,13 +959,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     const uint32_t tO = tS + BN;
     const float sl2 = a.scale_log2;
     const f32x2 scale2 = pair(sl2, sl2);
-    uint32_t gs = 0, oc = 0;                   // steps and items of this tile
+    uint32_t gs = 0, oc = 0, pos = 0;          // steps and items of this tile; steps of all
+    const int inc = spread ? NT : 1;
+    int q0 = 0, slot = 0;                      // Q slots: the item's first, this tile's last
     bool pending = false;                      // O of the item before is on its way out of its Q slot
     // Hands that slot to the loader once the store has read it.
     auto release_slot = [&]() {
       if (lane == 0 && pending) {
         bulk_wait_read();
-        mbar_arrive(q_empty + X * QB + (oc - 1) % QB);
+        mbar_arrive(q_empty + (K::TIGHT ? slot : 2 * X + int((oc - 1) & 1)));
       }
       pending = false;
     };
@@ -930,12 +979,17 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const Item &it = *ip;                    // handed back at the end
       const int n_kv = it.n_kv, n0 = it.n0, n1 = it.n1, s0 = it.s0, j0 = it.j0;
       if (it.n_qt == 0) break;
+      const int first = first_step<NT>(spread, pos, X);
+      const int mine = K::TIGHT ? q_slot(q0, q_index(spread, first, X), nq) : 2 * X + int(oc & 1);
+      if (K::TIGHT) q0 = q_slot(q0, q_tiles(spread, it.n_qt, n_kv), nq);
+      pos += n_kv;
+      if (X >= it.n_qt || first >= n_kv) release_slot();   // (no first step to do it at)
       if (X >= it.n_qt) {
         rd.done(item_empty, lane);
         continue;
       }
       float m = NO_KEY, l = 0.f;
-      for (int j = 0; j < n_kv; ++j, ++gs) {
+      for (int j = first; j < n_kv; j += inc, ++gs) {
         const int g = j0 + j < s0 ? 0 : 1, key0 = (g ? j0 + j - s0 : j0 + j) * BN;
         const int valid = (g ? n1 : n0) - key0;
         const unsigned char *mk = a.c.seg[g].mask;
@@ -975,7 +1029,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                            __uint_as_float(sr[c >> 1][(c & 1) * 8 + 2 * e + 1]));
         // a step without any key leaves the row at NO_KEY: its weights are 0
         const float mx = fmaxf(fmaxf(fmax3(mxp[0], mxp[1], mxp[2]), mxp[3]) * sl2, NO_KEY);
-        if (j == 0) {
+        if (j == first) {
           m = mx;
         } else {
           const bool need = mx > m + 8.0f;
@@ -1026,17 +1080,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(p_full + X);
-        if (j == 0) release_slot();
+        if (j == first) release_slot();
       }
       if (!ok) break;
       // O of the item: divided by the row sum, written out.  P of the next item
       // follows in this warp, so its PV cannot overwrite O before it is read.
-      const bool some = n_kv > 0;
+      const bool some = first < n_kv;
       const bool tma = a.tma_out && some;      // (an item without keys has no slot)
-      const int row = it.r0 + X * a.tile_rows + r;           // row of the unit
+      const int row = it.r0 + (spread ? 0 : X * a.tile_rows) + r;   // row of the unit
       const bool valid = r < a.tile_rows && row < a.c.R;
+      const int part = spread ? it.split * NT + X : it.split;
       float inv = 0.f, lse = -INFINITY;
-      uint8_t *stg = sQ + (X * QB + oc % QB) * K::QTILE;
+      uint8_t *stg = sQ + (K::TIGHT ? mine : 2 * X + int(oc & 1)) * K::QTILE;
       if (some) {
         if (!(ok = mbar_wait(o_full + X, oc & 1, epoch))) break;
         ++oc;
@@ -1046,7 +1101,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       char *out = nullptr;
       bool f32 = false;
       if (!tma && valid) {
-        const long long prow = (long long)it.split * a.c.part_rows + ((long long)it.unit * a.c.HW + it.w) * a.c.R + row;
+        const long long prow = (long long)part * a.c.part_rows + ((long long)it.unit * a.c.HW + it.w) * a.c.R + row;
         f32 = a.c.part_o || a.c.o_f32;
         out = a.c.part_o ? reinterpret_cast<char *>(a.c.part_o + prow * D)
                          : static_cast<char *>(a.c.o) + st::cond_row(a.c, it.unit, it.w, row) * (f32 ? 4 : 2);
@@ -1116,6 +1171,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       }
       if (some) {
         pending = true;
+        slot = mine;
         if (tma) {
           fence_async_smem();
           __syncwarp();
@@ -1131,7 +1187,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       }
       if (valid) {
         if (a.c.part_o)
-          a.c.part_lse[(long long)it.split * a.c.part_rows + ((long long)it.unit * a.c.HW + it.w) * a.c.R + row] = lse;
+          a.c.part_lse[(long long)part * a.c.part_rows + ((long long)it.unit * a.c.HW + it.w) * a.c.R + row] = lse;
         else if (a.c.lse) a.c.lse[st::cond_lse(a.c, it.unit, it.w, row)] = lse;
       }
       rd.done(item_empty, lane);
@@ -1221,12 +1277,14 @@ template <int D> st_status launch(const st::CondParams &p, cudaStream_t s) {
   Args a = {};
   a.c = p;
   a.tile_rows = BLOCK_M / p.G * p.G;
+  a.spread = p.spread > 1 ? 1 : 0;
+  a.n_split = p.n_split / p.spread;
   a.q_blocks = (p.R + K::NT * a.tile_rows - 1) / (K::NT * a.tile_rows);
-  const long long items = (long long)st::cond_units(p) * p.HW * p.n_split * a.q_blocks;
+  const long long items = (long long)st::cond_units(p) * p.HW * a.n_split * a.q_blocks;
   if (items > 0x3fffffffLL) return ST_ERR_SHAPE;
   a.n_items = int(items);
   a.dqb = st::make_fastdiv(uint32_t(a.q_blocks));
-  a.dsplit = st::make_fastdiv(uint32_t(p.n_split));
+  a.dsplit = st::make_fastdiv(uint32_t(a.n_split));
   a.dhw = st::make_fastdiv(uint32_t(p.HW));
   a.dkv = st::make_fastdiv(uint32_t(p.hdiv));
   a.dt = st::make_fastdiv(uint32_t(p.g.T));
@@ -1245,9 +1303,10 @@ template <int D> st_status launch(const st::CondParams &p, cudaStream_t s) {
         !map_kv(&m.v[g], sg.v, p, sg, K::VW, K::VSW, K::BN))
       return ST_ERR_CUDA;
   }
-  if (steps * (p.n_split + 1) >= (1LL << 31)) return ST_ERR_SHAPE;
+  if (steps * (a.n_split + 1) >= (1LL << 31)) return ST_ERR_SHAPE;
   a.max_steps = int(steps);
   a.resident = p.n_split == 1 && steps <= K::NSV ? 1 : 0;
+  a.nq = K::TIGHT && steps > 1 ? K::NQ - 1 : K::NQ;
   a.tma_out = !p.part_o && !p.o_f32 && p.G == 1 ? 1 : 0;
   if (!map_q(&m.q0, p.q, p, K::C0, K::SW0, a.tile_rows) ||
       (K::C1 && !map_q(&m.q1, p.q, p, K::C1X, K::SW1X, a.tile_rows)) ||
@@ -1303,7 +1362,7 @@ unsigned int read_and_clear_cond_error(cudaStream_t stream, cudaError_t *err) {
 }
 
 CondTile cond_tile(int D) {
-  return D <= 96 ? CondTile{3 * 128, D <= 64 ? 96 : (D <= 80 ? 80 : 64)} : CondTile{2 * 128, 128};
+  return D <= 96 ? CondTile{128, 3, D <= 64 ? 96 : (D <= 80 ? 80 : 64)} : CondTile{128, 2, 128};
 }
 
 st_status cond_sm100(const CondParams &p, cudaStream_t s) {
