@@ -94,25 +94,28 @@ template <int D> struct Cfg {
   static_assert(!DENSE || BLOCK_M * 2 * D <= QTILE, "O over Q");
   static constexpr int TABLE = D == 128 ? 32 : 64;     // key ranges of a segment held in shared memory
   static constexpr int TAIL = 2 * TABLE * 8 + 512 + (D == 128 ? 512 : 768);    // key ranges, items, barriers
-  static constexpr int ROOM = 232448 - 1024 - TAIL - NQ * QTILE;
-  // K and V stages: as many of both as fit, at most 8; an odd K tile more
-  static constexpr int NSV = TIGHT ? 2 : (ROOM / (KTILE + VTILE) > 8 ? 8 : ROOM / (KTILE + VTILE));
-  static constexpr int NSK = !TIGHT && NSV < 8 && ROOM - NSV * (KTILE + VTILE) >= KTILE ? NSV + 1 : NSV;
-  // streaming uses a multiple of NT: with the keys of an item spread over the
-  // tiles, a stage then belongs to one tile
-  static constexpr int SSK = NSK / NT * NT, SSV = NSV / NT * NT;
-  static constexpr int KV_BYTES = NSK * KTILE + NSV * VTILE;
-  static constexpr int SMEM = 1024 + (NQ - TIGHT) * QTILE + KV_BYTES + TAIL;
-  static_assert(SMEM <= 232448 && SSK >= NT && SSV >= NT, "shared memory");
-  static_assert(!TIGHT || (KTILE == QTILE && VTILE == QTILE), "a Q tile gives way to a K/V tile");
+  // K and V stages: as many of both as fit behind the Q tiles, at most NB.  Of
+  // the items of a spread launch (below) only one is in flight: NT Q tiles, and
+  // more stages.  The barriers of a step are counted apart from its stage, NB of
+  // them: a multiple of NT, so that with the steps dealt out to the tiles a
+  // barrier belongs to one tile, which sees every phase of it.
+  static constexpr int NB = TIGHT ? 2 : 6;
+  static constexpr int SMEM = 232448, ROOM = SMEM - 1024 - TAIL;
+  __host__ __device__ static constexpr int stages(int nq) {
+    const int n = (ROOM - nq * QTILE) / (KTILE + VTILE);
+    return n < NB ? n : NB;
+  }
+  static_assert(NB % NT == 0 && stages(NQ - TIGHT) >= 2 && (TIGHT || stages(NT) >= NT), "stages");
   // warps: softmax and epilogue of the tiles, then loader, issuers, V helper;
   // the rest of the last two warpgroups idles
   static constexpr int W_LOAD = 4 * NT, W_MMA = W_LOAD + 1, W_FIX = W_MMA + NT;
+  static constexpr int NF = NT == 3 ? 3 : 1;           // V helpers (as many as stay on whole barriers: NB % NF == 0)
   static constexpr int MISC = NT == 3 ? 8 : 4;
+  static_assert(NB % NF == 0 && 1 + NT + NF <= MISC, "helpers");
   static constexpr int THREADS = 32 * (W_LOAD + MISC);
   // registers: granted at launch, then moved to the softmax (setmaxnreg)
   static constexpr int R_LAUNCH = NT == 3 ? 96 : 168;
-  static constexpr int R_SOFT = NT == 3 ? 120 : 208, R_MISC = NT == 3 ? 56 : 88;
+  static constexpr int R_SOFT = NT == 3 ? 128 : 208, R_MISC = NT == 3 ? 48 : 88;
   static_assert(128 * NT * R_SOFT + 32 * MISC * R_MISC <= THREADS * R_LAUNCH, "register split");
 };
 
@@ -235,6 +238,9 @@ __device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {
   }
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1,
                                             int c2, int c3, int c4) {
   asm volatile(
@@ -378,7 +384,8 @@ struct Args {
   int resident;                // every key tile of an item fits the ring: K and V stay from item to item
   int max_steps;
   int spread;                  // the tiles of a CTA take the same rows and every NT-th step
-  int nq;                      // TIGHT: Q slots
+  int nq, ns;                  // Q slots, K and V stages
+  st::FastDiv dns;
   int n_split;                 // parts of an item's keys (each NT of the call's parts with spread)
   int tma_out;                 // bf16 rows go out as tiles
   float scale_log2;
@@ -541,13 +548,16 @@ struct Reader {
 
 // Position of the K/V ring: streaming, steps follow one another; resident,
 // step j is in stage j and `run` counts the loads of each.
-struct Ring {
+template <int NB> struct Ring {
   uint32_t pos = 0, run = 0;
-  template <int NS> __device__ __forceinline__ int stage(bool resident, int j) const {
-    return resident ? j : int((pos + j) % NS);
+  // barriers and their phase
+  __device__ __forceinline__ int bar(bool resident, int j) const { return resident ? j : int((pos + j) % NB); }
+  __device__ __forceinline__ uint32_t phase(bool resident, int j) const {
+    return (resident ? run : (pos + j) / NB) & 1;
   }
-  template <int NS> __device__ __forceinline__ uint32_t phase(bool resident, int j) const {
-    return (resident ? run : (pos + j) / NS) & 1;
+  __device__ __forceinline__ int stage(const Args &a, bool resident, int j) const {
+    const uint32_t x = pos + j;
+    return resident ? j : int(x - st::fdiv(x, a.dns) * uint32_t(a.ns));
   }
 };
 
@@ -565,45 +575,46 @@ __device__ __forceinline__ int q_index(bool spread, int first, int X) { return s
 __device__ __forceinline__ int q_tiles(bool spread, int n_qt, int n_kv) {
   return spread ? min(n_qt, n_kv) : (n_kv > 0 ? n_qt : 0);
 }
-// Slot `i` of the Q tiles after slot q0.
+// Its n-th Q tile's slot where each tile has its own.
+__device__ __forceinline__ int own_slot(bool spread, int X, uint32_t n) { return spread ? X : 2 * X + int(n & 1); }
+// TIGHT: slot `i` of the Q tiles after slot q0.
 __device__ __forceinline__ int q_slot(int q0, int i, int nq) { return q0 + i >= nq ? q0 + i - nq : q0 + i; }
 
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     cond_attn_sm100(const __grid_constant__ Maps mp, const __grid_constant__ Args a) {
   using K = Cfg<D>;
-  constexpr int NT = K::NT, NSK = K::NSK, NSV = K::NSV, NQ = K::NQ, BN = K::BN;
+  constexpr int NT = K::NT, NB = K::NB, NQ = K::NQ, BN = K::BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sQ = base;
-  const int nq = K::TIGHT ? a.nq : NQ;       // Q slots; K tiles behind them, then V tiles
+  const int nq = a.nq;
   uint8_t *sK = sQ + nq * K::QTILE;
-  uint8_t *sV = sK + (K::TIGHT ? NQ + 1 - nq : NSK) * K::KTILE;
-  int2 *sSet = reinterpret_cast<int2 *>(sQ + (NQ - K::TIGHT) * K::QTILE + K::KV_BYTES);
+  uint8_t *sV = sK + a.ns * K::KTILE;
+  int2 *sSet = reinterpret_cast<int2 *>(sQ + K::ROOM);
   Item *sItem = reinterpret_cast<Item *>(sSet + 2 * K::TABLE);
   uint64_t *bars = reinterpret_cast<uint64_t *>(sItem + ITEMS);
   uint64_t *q_full = bars, *q_empty = q_full + NQ;   // q_full: two per tile, its Q tiles in turn; q_empty: by slot
-  uint64_t *k_full = q_empty + NQ, *k_empty = k_full + NSK;      // k_empty, v_empty: one arrival per tile that reads the stage
-  uint64_t *v_full = k_empty + NSK, *v_empty = v_full + NSV, *v_ready = v_empty + NSV;
+  uint64_t *k_full = q_empty + NQ, *k_empty = k_full + NB;      // k_empty, v_empty: one arrival per tile that reads the stage
+  uint64_t *v_full = k_empty + NB, *v_empty = v_full + NB, *v_ready = v_empty + NB;
   // per tile: S ready; P written; O of an item complete
-  uint64_t *s_full = v_ready + NSV, *p_full = s_full + NT, *o_full = p_full + NT;
+  uint64_t *s_full = v_ready + NB, *p_full = s_full + NT, *o_full = p_full + NT;
   uint64_t *mma_done = o_full + NT;
   uint64_t *item_full = mma_done + NT, *item_empty = item_full + ITEMS;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(item_empty + ITEMS);
 
+  const bool resident = a.resident != 0, spread = a.spread != 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NQ; ++i) {
       mbar_init(q_full + i, 1);
       mbar_init(q_empty + i, 4);             // the softmax warps, once O is out of it
     }
-    for (int i = 0; i < NSK; ++i) {
+    for (int i = 0; i < NB; ++i) {
       mbar_init(k_full + i, 1);
-      mbar_init(k_empty + i, a.spread ? 1 : NT);
-    }
-    for (int i = 0; i < NSV; ++i) {
+      mbar_init(k_empty + i, spread ? 1 : NT);
       mbar_init(v_full + i, 1);
-      mbar_init(v_empty + i, a.spread ? 1 : NT);
+      mbar_init(v_empty + i, spread ? 1 : NT);
       mbar_init(v_ready + i, 1);
     }
     for (int i = 0; i < NT; ++i) {
@@ -614,7 +625,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     }
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_empty + i, 5 * NT + 1);   // softmax warps, issuers, helper
+      mbar_init(item_empty + i, 5 * NT + K::NF);   // softmax warps, issuers, helpers
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -623,6 +634,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                  "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (threadIdx.x == 32 * (K::W_LOAD + 1)) {   // (maps are parameters: nothing to wait for)
+    prefetch_map(&mp.q0);
+    if (K::C1) prefetch_map(&mp.q1);
+    if (a.c.seg[0].L) {
+      prefetch_map(&mp.k0[0]);
+      if (K::C1) prefetch_map(&mp.k1[0]);
+      prefetch_map(&mp.v[0]);
+    }
   }
   // barriers and TMEM are set up: let the next kernel of the stream be
   // scheduled, then wait for the previous one before any global access
@@ -642,7 +662,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t epoch = a.epoch;
-  const bool resident = a.resident != 0, spread = a.spread != 0;
 
   if (warp >= K::W_LOAD) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K::R_MISC));
@@ -651,7 +670,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       // An item is handed out once the next one is known, then loaded.
       if (lane == 0) {
         bool ok = true;
-        Ring ring;
+        Ring<NB> ring;
         uint32_t qn = 0;                              // 2 bits per tile: its Q tiles so far (barrier, phase)
         int last_kv = -1;                             // streaming: ring position of the last K/V issued
         int loaded = 0;                               // resident: stages loaded in this run
@@ -668,8 +687,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             const int X = spread ? int((ring.pos + i) % NT) : i;
             const uint32_t n = qn >> 2 * X & 3;
             uint64_t *full = q_full + 2 * X + (n & 1);
-            const int slot = K::TIGHT ? q0 : 2 * X + int(n & 1);
-            if (!(ok = mbar_wait(q_empty + slot, K::TIGHT ? q_phase : (n >> 1) ^ 1, epoch))) return false;
+            const int slot = K::TIGHT ? q0 : own_slot(spread, X, n);
+            const uint32_t ph = K::TIGHT ? q_phase : ((spread ? n : n >> 1) & 1) ^ 1;
+            if (!(ok = mbar_wait(q_empty + slot, ph, epoch))) return false;
             qn ^= (n ^ ((n + 1) & 3)) << 2 * X;
             uint8_t *dst = sQ + slot * K::QTILE;
             if (K::TIGHT && ++q0 == nq) {
@@ -723,35 +743,40 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           first = false;
           const int n = resident ? (load_kv ? a.max_steps : 1) : it.n_kv;
           for (int j = 0; j < n && ok; ++j) {
-            const int sk = ring.stage<K::SSK>(resident, j), sv = ring.stage<K::SSV>(resident, j);
+            const int bar = ring.bar(resident, j), st = ring.stage(a, resident, j);
+            // the stage is free once the step before it there has been read
+            const uint32_t before = ring.pos + j - a.ns;
+            const int was = resident ? j : int(before % NB);
+            const uint32_t ph = resident ? (ring.run & 1) ^ 1 : before / NB & 1;
+            const bool wait = resident || int(ring.pos + j) >= a.ns;
             const Step sp = step_of<BN>(it, j);
             const int g = sp.seg;
             const int set = a.c.seg[g].offsets ? 0 : sp.set;   // packed: rows of one long sequence
             const bool real = j < it.n_kv;            // resident: stages past the item's steps only change phase
             if (load_kv) {
-              if (!(ok = mbar_wait(k_empty + sk, ring.phase<K::SSK>(resident, j) ^ 1, epoch))) break;
+              if (wait && !(ok = mbar_wait(k_empty + was, ph, epoch))) break;
               if (real) {
-                mbar_expect_tx(k_full + sk, K::KBYTES);
-                uint8_t *dk = sK + sk * K::KTILE;
-                tma_load_4d(dk, &mp.k0[g], k_full + sk, 0, it.kvh, sp.row + sp.key, set);
-                if (K::C1) tma_load_4d(dk + K::KT0, &mp.k1[g], k_full + sk, 64, it.kvh, sp.row + sp.key, set);
+                mbar_expect_tx(k_full + bar, K::KBYTES);
+                uint8_t *dk = sK + st * K::KTILE;
+                tma_load_4d(dk, &mp.k0[g], k_full + bar, 0, it.kvh, sp.row + sp.key, set);
+                if (K::C1) tma_load_4d(dk + K::KT0, &mp.k1[g], k_full + bar, 64, it.kvh, sp.row + sp.key, set);
                 if (!resident) last_kv = int(ring.pos) + j;
                 else loaded = j + 1;
               } else {
-                mbar_arrive(k_full + sk);
+                mbar_arrive(k_full + bar);
               }
             }
             if (j == 0 && !load_q(it, 0, tight ? 1 : NT)) break;
             if (load_kv) {
-              if (!(ok = mbar_wait(v_empty + sv, ring.phase<K::SSV>(resident, j) ^ 1, epoch))) break;
+              if (wait && !(ok = mbar_wait(v_empty + was, ph, epoch))) break;
               if (real) {
-                mbar_expect_tx(v_full + sv, K::VTILE);
-                uint8_t *dv = sV + sv * K::VTILE;
+                mbar_expect_tx(v_full + bar, K::VTILE);
+                uint8_t *dv = sV + st * K::VTILE;
 #pragma unroll 1
                 for (int t = 0; t < K::VA; ++t)
-                  tma_load_4d(dv + t * K::VAT, &mp.v[g], v_full + sv, t * K::VW, it.kvh, sp.row + sp.key, set);
+                  tma_load_4d(dv + t * K::VAT, &mp.v[g], v_full + bar, t * K::VW, it.kvh, sp.row + sp.key, set);
               } else {
-                mbar_arrive(v_full + sv);
+                mbar_arrive(v_full + bar);
               }
             }
             if (tight && j == (n > 1 ? 1 : 0) && !load_q(it, 1, NT)) break;
@@ -768,8 +793,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
               mbar_drain(v_full + j, ring.run & 1);
             }
           } else {
-            for (int i = last_kv; i >= 0 && i > last_kv - K::SSK; --i) mbar_drain(k_full + i % K::SSK, (i / K::SSK) & 1);
-            for (int i = last_kv; i >= 0 && i > last_kv - K::SSV; --i) mbar_drain(v_full + i % K::SSV, (i / K::SSV) & 1);
+            for (int i = last_kv; i >= 0 && i > last_kv - NB; --i) mbar_drain(k_full + i % NB, (i / NB) & 1);
+            for (int i = last_kv; i >= 0 && i > last_kv - NB; --i) mbar_drain(v_full + i % NB, (i / NB) & 1);
           }
           for (int X = 0; X < NT; ++X)
             for (uint32_t k = 1; k <= 2; ++k) {       // (a barrier never used answers at once)
@@ -789,7 +814,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const uint32_t dS = uniform(tmem) + X * K::TW, dO = dS + BN;
       const uint32_t lead = elect_one();
       bool ok = true;
-      Ring ring;
+      Ring<NB> ring;
       Reader rd;
       uint32_t qc = 0, steps = 0;                      // Q tiles and steps of this tile so far
       int q0 = 0;                                      // first Q slot of the item
@@ -824,19 +849,20 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const int j0 = first_step<NT>(spread, ring.pos, X), inc = spread ? NT : 1;
         const bool here = X < cur.n_qt && j0 < cur.n;
         if (here) {
-          const int slot = K::TIGHT ? q_slot(q0, q_index(spread, j0, X), nq) : 2 * X + int(qc & 1);
+          const int slot = K::TIGHT ? q_slot(q0, q_index(spread, j0, X), nq) : own_slot(spread, X, qc);
           const uint32_t qa = sdesc_lo<16>(aQ + slot * K::QTILE);
           if (!(ok = mbar_wait(q_full + 2 * X + (qc & 1), (qc >> 1) & 1, epoch))) break;
           ++qc;
           for (int j = j0; j < cur.n; j += inc, ++steps) {
             // S(j), over P(j - 1), which PV(j - 1) has read by then; only as many
             // keys as there are (whole chunks)
-            const int sk = ring.stage<K::SSK>(resident, j), sv = ring.stage<K::SSV>(resident, j);
-            if (cur.fresh && !(ok = mbar_wait(k_full + sk, ring.phase<K::SSK>(resident, j), epoch))) break;
+            const int bar = ring.bar(resident, j), st = ring.stage(a, resident, j);
+            const uint32_t ph = ring.phase(resident, j);
+            if (cur.fresh && !(ok = mbar_wait(k_full + bar, ph, epoch))) break;
             tc_fence_after();
             const int nk = cur.chunks(j);
             const uint32_t ids = idesc_bf16(BLOCK_M, 0, 0, 0) | uint32_t(nk * 2) << 17;
-            const uint32_t ka = sdesc_lo<16>(aK + sk * K::KTILE);
+            const uint32_t ka = sdesc_lo<16>(aK + st * K::KTILE);
 #pragma unroll
             for (int kk = 0; kk < K::C0 / 16; ++kk)
               mma_ss(lead, dS, sdesc<8 * K::SW0, layout_of(K::SW0)>(qa + kk * 2),
@@ -848,12 +874,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                        sdesc<8 * K::SW1X, layout_of(K::SW1X)>(ka + K::KT0 / 16 + kk * 2), ids, 1);
             }
             tc_commit(lead, s_full + X);
-            if (cur.release) tc_commit(lead, k_empty + sk);  // handed back at the last item that reads it
+            if (cur.release) tc_commit(lead, k_empty + bar);  // handed back at the last item that reads it
             // PV(j)
-            if (cur.fresh && !(ok = mbar_wait(v_ready + sv, ring.phase<K::SSV>(resident, j), epoch))) break;
+            if (cur.fresh && !(ok = mbar_wait(v_ready + bar, ph, epoch))) break;
             const bool last = j + inc >= cur.n;
             if (last && !(ok = fetch())) break;              // wk: now the next item
-            const uint32_t va = sdesc_lo<K::VAT>(aV + sv * K::VTILE);
+            const uint32_t va = sdesc_lo<K::VAT>(aV + st * K::VTILE);
             if (!(ok = mbar_wait(p_full + X, steps & 1, epoch))) break;
             tc_fence_after();
             constexpr uint32_t IDPV = idesc_bf16(BLOCK_M, K::DPV, 0, 1);
@@ -863,7 +889,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 mma_ts(lead, dO, dS + kk * 8, sdesc<8 * K::VSW, layout_of(K::VSW)>(va + kk * K::VSW), IDPV,
                        (j > j0 || kk > 0) ? 1u : 0u);
             if (last) tc_commit(lead, o_full + X);
-            if (cur.release) tc_commit(lead, v_empty + sv);
+            if (cur.release) tc_commit(lead, v_empty + bar);
           }
           if (!ok) break;
         }
@@ -872,11 +898,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (cur.release && !spread) {
           const int last = resident ? a.max_steps : cur.n;
           for (int j = here ? cur.n : 0; j < last && ok; ++j) {
-            const int sk = ring.stage<K::SSK>(resident, j), sv = ring.stage<K::SSV>(resident, j);
-            if (!(ok = mbar_wait(k_full + sk, ring.phase<K::SSK>(resident, j), epoch))) break;
-            tc_commit(lead, k_empty + sk);
-            if (!(ok = mbar_wait(v_ready + sv, ring.phase<K::SSV>(resident, j), epoch))) break;
-            tc_commit(lead, v_empty + sv);
+            const int bar = ring.bar(resident, j);
+            const uint32_t ph = ring.phase(resident, j);
+            if (!(ok = mbar_wait(k_full + bar, ph, epoch))) break;
+            tc_commit(lead, k_empty + bar);
+            if (!(ok = mbar_wait(v_ready + bar, ph, epoch))) break;
+            tc_commit(lead, v_empty + bar);
           }
         }
         if (K::TIGHT) q0 = q_slot(q0, q_tiles(spread, cur.n_qt, cur.n), nq);
@@ -890,11 +917,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       tc_commit(lead, mma_done + X);
       mbar_drain(mma_done + X, 0);
       __syncwarp();
-    } else if (warp == K::W_FIX) {
+    } else if (warp >= K::W_FIX && warp < K::W_FIX + K::NF) {
       // ================= V rows of keys that do not count; ones column =================
       constexpr int A1 = K::ONES ? D / K::VW : 0, XB = (D % K::VW) * 2;
       bool ok = true;
-      Ring ring;
+      Ring<NB> ring;
       Reader rd;
       bool first = true;
       while (ok) {
@@ -907,9 +934,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (resident && !first) ++ring.run;
         first = false;
         const int n = resident ? a.max_steps : it.n_kv;
-        for (int j = 0; j < n; ++j) {
-          const int st = ring.stage<K::SSV>(resident, j);
-          const uint32_t ph = ring.phase<K::SSV>(resident, j);
+        // its steps: those whose barrier is one of its own
+        int j = warp - K::W_FIX - (resident ? 0 : int(ring.pos % K::NF));
+        if (j < 0) j += K::NF;
+        for (; j < n; j += K::NF) {
+          const int bar = ring.bar(resident, j), st = ring.stage(a, resident, j);
+          const uint32_t ph = ring.phase(resident, j);
           const Step sp = step_of<BN>(it, j);
           const unsigned char *mk = a.c.seg[sp.seg].mask;
           const bool work = j < it.n_kv && (K::ONES || sp.valid < BN || mk);
@@ -922,7 +952,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
               keep[i] = r < sp.valid && (!mk || st::after_wait(mk)[r]);
             }
           }
-          if (lane == 0) ok = mbar_wait(v_full + st, ph, epoch);
+          if (lane == 0) ok = mbar_wait(v_full + bar, ph, epoch);
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
           if (!ok) break;
           if (work) {
@@ -944,7 +974,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             fence_async_smem();                // visible to the tensor core
             __syncwarp();
           }
-          if (lane == 0) mbar_arrive(v_ready + st);
+          if (lane == 0) mbar_arrive(v_ready + bar);
         }
         if (!resident) ring.pos += it.n_kv;
       }
@@ -967,7 +997,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     auto release_slot = [&]() {
       if (lane == 0 && pending) {
         bulk_wait_read();
-        mbar_arrive(q_empty + (K::TIGHT ? slot : 2 * X + int((oc - 1) & 1)));
+        mbar_arrive(q_empty + (K::TIGHT ? slot : own_slot(false, X, oc - 1)));
       }
       pending = false;
     };
@@ -980,7 +1010,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const int n_kv = it.n_kv, n0 = it.n0, n1 = it.n1, s0 = it.s0, j0 = it.j0;
       if (it.n_qt == 0) break;
       const int first = first_step<NT>(spread, pos, X);
-      const int mine = K::TIGHT ? q_slot(q0, q_index(spread, first, X), nq) : 2 * X + int(oc & 1);
+      const int mine = K::TIGHT ? q_slot(q0, q_index(spread, first, X), nq) : own_slot(spread, X, oc);
       if (K::TIGHT) q0 = q_slot(q0, q_tiles(spread, it.n_qt, n_kv), nq);
       pos += n_kv;
       if (X >= it.n_qt || first >= n_kv) release_slot();   // (no first step to do it at)
@@ -1091,7 +1121,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const bool valid = r < a.tile_rows && row < a.c.R;
       const int part = spread ? it.split * NT + X : it.split;
       float inv = 0.f, lse = -INFINITY;
-      uint8_t *stg = sQ + (K::TIGHT ? mine : 2 * X + int(oc & 1)) * K::QTILE;
+      uint8_t *stg = sQ + mine * K::QTILE;
       if (some) {
         if (!(ok = mbar_wait(o_full + X, oc & 1, epoch))) break;
         ++oc;
@@ -1170,9 +1200,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         }
       }
       if (some) {
-        pending = true;
-        slot = mine;
         if (tma) {
+          pending = true;
+          slot = mine;
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -1183,6 +1213,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             }
             bulk_commit();
           }
+        } else if (lane == 0) {
+          mbar_arrive(q_empty + mine);         // Q was read, nothing is staged over it
         }
       }
       if (valid) {
@@ -1305,8 +1337,10 @@ template <int D> st_status launch(const st::CondParams &p, cudaStream_t s) {
   }
   if (steps * (a.n_split + 1) >= (1LL << 31)) return ST_ERR_SHAPE;
   a.max_steps = int(steps);
-  a.resident = p.n_split == 1 && steps <= K::NSV ? 1 : 0;
-  a.nq = K::TIGHT && steps > 1 ? K::NQ - 1 : K::NQ;
+  a.nq = K::TIGHT ? K::NQ - (steps > 1) : (a.spread ? K::NT : K::NQ);
+  a.ns = K::stages(a.nq);
+  a.dns = st::make_fastdiv(uint32_t(a.ns));
+  a.resident = p.n_split == 1 && steps <= a.ns ? 1 : 0;
   a.tma_out = !p.part_o && !p.o_f32 && p.G == 1 ? 1 : 0;
   if (!map_q(&m.q0, p.q, p, K::C0, K::SW0, a.tile_rows) ||
       (K::C1 && !map_q(&m.q1, p.q, p, K::C1X, K::SW1X, a.tile_rows)) ||
