@@ -171,7 +171,7 @@ st_status make_plan(const st_attn_desc *desc, const st_kv_desc *d0, const st_kv_
 // The parts' weights exp(lse_c - M) (M the largest), the weighted rows, and
 // with OWN the row's own keys in the same softmax.  Parts whose LSE is -inf (no
 // key) are not read.  Bound by the latency of its chains of loads more than by
-// the bytes: WPR warps take a row (every WPR-th part and 32 keys), a lane holds
+// the bytes: WPR warps take a row (every WPR-th part and 16 keys), a lane holds
 // 4 consecutive channels, and the warps join over shared memory.
 __device__ __forceinline__ float4 load4(const uint16_t *p, int) {
   const uint2 v = *reinterpret_cast<const uint2 *>(p);
@@ -188,8 +188,10 @@ __device__ __forceinline__ void axpy4(float4 &a, float w, const float4 &x) {
   a.w = fmaf(w, x.w, a.w);
 }
 
+constexpr int BATCH = 8;       // loads of a lane in flight
+
 template <typename T, bool OWN, int WPR>
-__global__ void __launch_bounds__(128) cond_combine(const __grid_constant__ CondParams p) {
+__global__ void __launch_bounds__(128, WPR == 4 ? 8 : 4) cond_combine(const __grid_constant__ CondParams p) {
   __shared__ __align__(16) float sq[4][128];
   __shared__ float sm[4], sl[4];
   constexpr float L2E = 1.4426950408889634f;
@@ -224,17 +226,22 @@ __global__ void __launch_bounds__(128) cond_combine(const __grid_constant__ Cond
     const T *K = static_cast<const T *>(st::after_wait(sg.k)) + base;
     const T *V = static_cast<const T *>(st::after_wait(sg.v)) + base;
     const unsigned char *mk = sg.mask ? st::after_wait(sg.mask) + (long long)kr.set * sg.L : nullptr;
-    for (int k0 = 32 * sub; k0 < kr.n; k0 += 32 * WPR) {
-      const int key = k0 + lane;
-      float x = -INFINITY;
-      if (key < kr.n && (!mk || mk[key])) {    // one key per lane
+    for (int k0 = 16 * sub; k0 < kr.n; k0 += 16 * WPR) {
+      const int key = k0 + (lane >> 1), half = lane & 1;     // two lanes per key, every other 8 channels each
+      float x = 0.f;
+      const bool on = key < kr.n && (!mk || mk[key]);
+      if (on) {
         const T *kp = K + (long long)key * sg.stride_l;
-        x = 0.f;
         if constexpr (sizeof(T) == 2) {
-#pragma unroll 4
-          for (int d = 0; d < D; d += 8) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(kp + d);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+          uint4 v[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (16 * c + 8 * half < D) v[c] = *reinterpret_cast<const uint4 *>(kp + 16 * c + 8 * half);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int d = 16 * c + 8 * half;
+            if (d >= D) break;
+            const uint32_t u[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               x = fmaf(sq[wp][d + 2 * i], __uint_as_float(u[i] << 16), x);
@@ -243,9 +250,11 @@ __global__ void __launch_bounds__(128) cond_combine(const __grid_constant__ Cond
           }
         } else {
 #pragma unroll 8
-          for (int d = 0; d < D; ++d) x = fmaf(sq[wp][d], kp[d], x);
+          for (int d = half; d < D; d += 2) x = fmaf(sq[wp][d], kp[d], x);
         }
       }
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      if (!on) x = -INFINITY;
       float mx = x;
 #pragma unroll
       for (int y = 16; y > 0; y >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
@@ -254,16 +263,21 @@ __global__ void __launch_bounds__(128) cond_combine(const __grid_constant__ Cond
       const float corr = exp2f(m - ref), e = exp2f(x - ref);
       float sum = e;
 #pragma unroll
-      for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+      for (int y = 16; y > 1; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
       l = l * corr + sum;
       m = mn;
       acc = make_float4(acc.x * corr, acc.y * corr, acc.z * corr, acc.w * corr);
       const unsigned counts = __ballot_sync(0xffffffffu, e != 0.f);
-      const int nk = min(32, kr.n - k0);
-#pragma unroll 8
-      for (int k = 0; k < nk; ++k) {           // a key that does not count is not read
-        const float pk = __shfl_sync(0xffffffffu, e, k);
-        if ((counts >> k & 1) && nd > 0) axpy4(acc, pk, load4(V + (long long)(k0 + k) * sg.stride_l + d0, nd));
+      const int nk = min(16, kr.n - k0);
+      for (int kb = 0; kb < nk; kb += BATCH) { // a key that does not count is not read
+        float4 x4[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          x4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (nd > 0 && (counts >> 2 * (kb + i) & 1)) x4[i] = load4(V + (long long)(k0 + kb + i) * sg.stride_l + d0, nd);
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) axpy4(acc, __shfl_sync(0xffffffffu, e, 2 * (kb + i)), x4[i]);
       }
     }
   }
@@ -284,14 +298,22 @@ __global__ void __launch_bounds__(128) cond_combine(const __grid_constant__ Cond
   for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
   sum += l * own;
   acc = make_float4(acc.x * own, acc.y * own, acc.z * own, acc.w * own);
-#pragma unroll 4
-  for (int i = 0; sub + WPR * i < n; ++i) {
-    const float wc = __shfl_sync(0xffffffffu, i < 32 ? w0 : w1, i & 31);
-    if (wc != 0.f && nd > 0) {
-      const float *src = part_o + ((long long)(sub + WPR * i) * p.part_rows + row) * D + d0;
-      if constexpr (sizeof(T) == 2) axpy4(acc, wc, *reinterpret_cast<const float4 *>(src));
-      else axpy4(acc, wc, load4(src, nd));
+  for (int b = 0; sub + WPR * b < n; b += BATCH) {
+    float4 x4[BATCH];
+    float wc[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int c = b + i;                     // (c <= 63; a part past the last has weight 0)
+      wc[i] = __shfl_sync(0xffffffffu, c < 32 ? w0 : w1, c & 31);
+      x4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (wc[i] != 0.f && nd > 0) {
+        const float *src = part_o + ((long long)(sub + WPR * c) * p.part_rows + row) * D + d0;
+        if constexpr (sizeof(T) == 2) x4[i] = *reinterpret_cast<const float4 *>(src);
+        else x4[i] = load4(src, nd);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) axpy4(acc, wc[i], x4[i]);
   }
   if constexpr (WPR > 1) {                     // join the warps of the row
     if (lane == 0) {
