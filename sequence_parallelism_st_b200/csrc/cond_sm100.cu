@@ -93,7 +93,7 @@ template <int D> struct Cfg {
   static constexpr bool DENSE = D == 72 || D == 80;
   static_assert(!DENSE || BLOCK_M * 2 * D <= QTILE, "O over Q");
   static constexpr int TABLE = D == 128 ? 32 : 64;     // key ranges of a segment held in shared memory
-  static constexpr int TAIL = 2 * TABLE * 8 + 512 + (D == 128 ? 512 : 768);    // key ranges, items, barriers
+  static constexpr int TAIL = 2 * TABLE * 8 + 384 + 512;    // key ranges, items, barriers and the TMEM slot
   // K and V stages: as many of both as fit behind the Q tiles, at most NB.  Of
   // the items of a spread launch (below) only one is in flight: NT Q tiles, and
   // more stages.  The barriers of a step are counted apart from its stage, NB of
@@ -111,6 +111,7 @@ template <int D> struct Cfg {
   static constexpr int W_LOAD = 4 * NT, W_MMA = W_LOAD + 1, W_FIX = W_MMA + NT;
   static constexpr int NF = NT == 3 ? 3 : 1;           // V helpers (as many as stay on whole barriers: NB % NF == 0)
   static constexpr int MISC = NT == 3 ? 8 : 4;
+  static_assert(8 * (2 * NQ + 5 * NB + 4 * NT + 8) + 4 <= 512, "barriers");
   static_assert(NB % NF == 0 && 1 + NT + NF <= MISC, "helpers");
   static constexpr int THREADS = 32 * (W_LOAD + MISC);
   // registers: granted at launch, then moved to the softmax (setmaxnreg)
@@ -381,6 +382,7 @@ struct Args {
   int band, band_last, cols, n_bands;
   st::FastDiv dband, dband_last, dbandcols;
   int n_items;
+  int weighed;                 // resident, sets of different lengths: items are cut by cost
   int resident;                // every key tile of an item fits the ring: K and V stay from item to item
   int max_steps;
   int spread;                  // the tiles of a CTA take the same rows and every NT-th step
@@ -409,7 +411,7 @@ struct alignas(16) Item {
   int pad[3];
 };
 constexpr int ITEMS = 4;       // items in flight between the scheduler and the others
-static_assert(ITEMS * sizeof(Item) <= 512, "item ring");
+static_assert(ITEMS * sizeof(Item) <= 384, "item ring");
 
 struct Step {
   int seg, key, valid;         // segment, first key in its range, keys that exist
@@ -433,8 +435,25 @@ template <int D> __device__ __forceinline__ void rows_of(const Args &a, Item &it
   it.n_qt = a.spread ? Cfg<D>::NT : left > 2 * a.tile_rows && Cfg<D>::NT > 2 ? 3 : (left > a.tile_rows ? 2 : 1);
 }
 
+// The keys of segment g that batch b attends.  table: the segments' ranges.
+template <int D>
+__device__ __forceinline__ void set_range(const Args &a, const int2 *table, int g, int b, int &set, int &row, int &n) {
+  set = row = n = 0;
+  if (g >= a.c.n_seg) return;
+  set = int(st::fdiv(uint32_t(b), a.dper[g]));
+  if (a.c.seg[g].n_sets <= Cfg<D>::TABLE) {
+    const int2 r = table[g * Cfg<D>::TABLE + set];
+    row = r.x;
+    n = r.y;
+  } else {
+    const st::KvRange r = st::kv_range(a.c.seg[g], b);
+    row = r.row0;
+    n = r.n;
+  }
+}
+
 // Streaming: q block fastest, then split, head, unit.  Resident: q block of a
-// band, head and unit, band.  table: the segments' key ranges (row, n).
+// band, head and unit, band.
 template <int D>
 __device__ __forceinline__ Item decode(const Args &a, const int2 *table, int x) {
   using K = Cfg<D>;
@@ -470,22 +489,8 @@ __device__ __forceinline__ Item decode(const Args &a, const int2 *table, int x) 
     it.c4 = ub;
   }
   const int b = ub * a.c.bm;
-  auto range = [&](int g, int &set, int &row, int &n) {
-    set = row = n = 0;
-    if (g >= a.c.n_seg) return;
-    set = int(st::fdiv(uint32_t(b), a.dper[g]));
-    if (a.c.seg[g].n_sets <= K::TABLE) {
-      const int2 r = table[g * K::TABLE + set];
-      row = r.x;
-      n = r.y;
-    } else {
-      const st::KvRange r = st::kv_range(a.c.seg[g], b);
-      row = r.row0;
-      n = r.n;
-    }
-  };
-  range(0, it.set0, it.row0, it.n0);
-  range(1, it.set1, it.row1, it.n1);
+  set_range<D>(a, table, 0, b, it.set0, it.row0, it.n0);
+  set_range<D>(a, table, 1, b, it.set1, it.row1, it.n1);
   it.s0 = (it.n0 + K::BN - 1) / K::BN;
   const int total = it.s0 + (it.n1 + K::BN - 1) / K::BN;
   if (a.n_split == 1) {
@@ -508,13 +513,46 @@ __device__ __forceinline__ bool same_keys(const Item &a, const Item &b) {
 // work on the same rows of the other heads, whose channels lie next to these
 // in Q and O: sectors that two heads share, and DRAM pages, are then touched
 // at about the same time.  (Heads at different rows at a time: Q and O of
-// 65,536 x 16 heads x 72 ran at 2.3 TB/s.)
-struct Walk {
+// 65,536 x 16 heads x 72 ran at 2.3 TB/s.)  Where the sets differ in length
+// the cut is by cost: an item without keys costs about as much as ITEM_STEPS
+// steps.
+constexpr int ITEM_STEPS = 2, WEIGHED = 16;      // units up to which the cut is by cost
+template <int D> struct Walk {
   int x, end, inc;
-  __device__ __forceinline__ explicit Walk(const Args &a) {
+  static __device__ __forceinline__ int cost(const Args &a, const int2 *table, int unit) {
+    const int b = int(st::fdiv(uint32_t(unit), a.dt)) * a.c.bm;
+    int set, row, n0, n1;
+    set_range<D>(a, table, 0, b, set, row, n0);
+    set_range<D>(a, table, 1, b, set, row, n1);
+    return ITEM_STEPS + (n0 + Cfg<D>::BN - 1) / Cfg<D>::BN + (n1 + Cfg<D>::BN - 1) / Cfg<D>::BN;
+  }
+  // first item of CTA `cta`
+  static __device__ int cut(const Args &a, const int2 *table, int units, uint32_t sum, int cta) {
+    const unsigned long long col = (unsigned long long)sum * a.c.HW;   // a row block of all heads
+    unsigned long long rest = col * a.q_blocks * cta / gridDim.x;
+    const int band = min(int(rest / (col * a.band)), a.n_bands - 1);
+    rest -= col * a.band * band;
+    const int len = band + 1 < a.n_bands ? a.band : a.band_last;
+    int z = 0;
+    for (int u = 0; u < units; ++u) {
+      const uint32_t c = cost(a, table, u);
+      const unsigned long long all = (unsigned long long)c * a.c.HW * len;
+      if (rest < all) return band * a.band * a.cols + z * len + int(rest / c);
+      rest -= all;
+      z += a.c.HW;
+    }
+    return band * a.band * a.cols + z * len;
+  }
+  __device__ __forceinline__ explicit Walk(const Args &a, const int2 *table) {
     if (a.resident) {
       inc = 1;
-      if (int(gridDim.x) >= a.n_bands * a.cols) {      // a band of a head per CTA
+      if (a.weighed) {
+        const int units = a.c.g.B * a.c.g.T;
+        uint32_t sum = 0;
+        for (int u = 0; u < units; ++u) sum += cost(a, table, u);
+        x = cut(a, table, units, sum, blockIdx.x);
+        end = cut(a, table, units, sum, blockIdx.x + 1);
+      } else if (int(gridDim.x) >= a.n_bands * a.cols) {   // a band of a head per CTA
         const int band = int(blockIdx.x) / a.cols, col = int(blockIdx.x) - band * a.cols;
         const int len = band + 1 < a.n_bands ? a.band : a.band_last;
         x = band * a.band * a.cols + col * len;
@@ -675,7 +713,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         int last_kv = -1;                             // streaming: ring position of the last K/V issued
         int loaded = 0;                               // resident: stages loaded in this run
         bool first = true;
-        Walk wk(a);
+        Walk<D> wk(a, sSet);
         const bool tight = K::TIGHT && nq < NQ;
         int q0 = 0;                                   // next Q slot
         uint32_t q_phase = 1;                         // parity its release shows
@@ -1356,7 +1394,9 @@ template <int D> st_status launch(const st::CondParams &p, cudaStream_t s) {
     // begin or end within
     a.cols = st::cond_units(p) * p.HW;
     const int share = (a.n_items + ctas - 1) / ctas;
-    const int whole = a.cols <= ctas ? (a.q_blocks + ctas / a.cols - 1) / (ctas / a.cols) : a.q_blocks + 1;
+    for (int g = 0; g < p.n_seg; ++g) a.weighed |= p.seg[g].n_sets > 1 && (p.seg[g].len || p.seg[g].offsets);
+    a.weighed = a.weighed && st::cond_units(p) <= WEIGHED;
+    const int whole = a.cols <= ctas && !a.weighed ? (a.q_blocks + ctas / a.cols - 1) / (ctas / a.cols) : a.q_blocks + 1;
     a.band = whole <= share ? whole : (share < a.q_blocks ? share : a.q_blocks);
     a.n_bands = (a.q_blocks + a.band - 1) / a.band;
     a.band_last = a.q_blocks - (a.n_bands - 1) * a.band;
