@@ -8,15 +8,42 @@
 // channels and their 4 partners, two 8-byte vectors), so a pair never crosses
 // lanes; a head is D / 8 consecutive lanes and a warp holds floor(32 / (D / 8))
 // heads of one token at a time.  The sum of squares runs over a head's lanes
-// with shuffles.  A warp task is UNROLL such groups of heads of one token,
-// loaded before any is used; the task's row of the table is read once for all
-// of them.  One token is spread over as many warps as it has groups, so a
-// single token costs one trip to memory.
+// with shuffles.  The heads of Q and K of a token are one list, cut into tasks
+// of two to four such groups; a warp has the loads of its next task in flight while
+// it works on one, and the sums of a task's groups run side by side.  Gains lie
+// in shared memory.
 #include "common.cuh"
 
 namespace {
 
-constexpr int UNROLL = 4;
+// Pairs of fp32 in 64-bit registers: one instruction for two products.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float x, float y) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(f32x2 a) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+  return d;
+}
+__device__ __forceinline__ f32x2 ffma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 fmul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// 1 / sqrt(x): the hardware's estimate and one Newton step (x = 0: infinite; NaN stays).
+__device__ __forceinline__ float inv_sqrt(float x) {
+  const float y = rsqrtf(x);
+  const float z = fmaf(0.5f * y, fmaf(-x * y, y, 1.f), y);
+  return x > 0.f && y < INFINITY ? z : y;
+}
 
 struct QkArgs {
   const void *q, *k;
@@ -25,9 +52,9 @@ struct QkArgs {
   const float *gq, *gk;
   const float4 *table;
   const int *positions;
-  int n_pos, period, n_tokens, hq, hk, D;
+  int n_pos, period, n_tokens, hq, heads, D;   // heads: of Q and K
   float eps;
-  int chunks_q, chunks;        // tasks of a token: of Q, in all
+  int chunks;                  // tasks of a token
   st::FastDiv dchunk, dperiod;
 };
 
@@ -44,13 +71,10 @@ template <bool HALVES> struct Lane8<uint16_t, HALVES> {
       b = make_uint2(v.z, v.w);
     }
   }
-  __device__ __forceinline__ void get(float *x) const {
+  __device__ __forceinline__ void get(f32x2 *x) const {
     const uint32_t w[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
   __device__ __forceinline__ static void store(uint16_t *p, int j, int half, const float *x) {
     const uint32_t w0 = st::pack_bf16x2(x[0], x[1]), w1 = st::pack_bf16x2(x[2], x[3]);
@@ -71,9 +95,11 @@ template <bool HALVES> struct Lane8<float, HALVES> {
     a = *reinterpret_cast<const float4 *>(p + first(j));
     b = *reinterpret_cast<const float4 *>(p + second(j, half));
   }
-  __device__ __forceinline__ void get(float *x) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  __device__ __forceinline__ void get(f32x2 *x) const {
+    x[0] = pair(a.x, a.y);
+    x[1] = pair(a.z, a.w);
+    x[2] = pair(b.x, b.y);
+    x[3] = pair(b.z, b.w);
   }
   __device__ __forceinline__ static void store(float *p, int j, int half, const float *x) {
     *reinterpret_cast<float4 *>(p + first(j)) = make_float4(x[0], x[1], x[2], x[3]);
@@ -81,97 +107,175 @@ template <bool HALVES> struct Lane8<float, HALVES> {
   }
 };
 
-template <typename T, bool HALVES, bool ROPE>
-__global__ void __launch_bounds__(256) qk_norm_rope(const __grid_constant__ QkArgs a) {
+// LPH: lanes of a head (D / 8), or 0 for any.  UNROLL: groups of a task.
+template <typename T, bool HALVES, bool ROPE, int LPH, int UNROLL>
+__global__ void __launch_bounds__(256, 3) qk_norm_rope(const __grid_constant__ QkArgs a) {
+  __shared__ __align__(16) float gains[2][256];
   const int lane = threadIdx.x & 31;
-  const int lph = a.D >> 3, hpw = 32 / lph;    // lanes of a head, heads of a warp
+  const int lph = LPH ? LPH : a.D >> 3, hpw = 32 / lph, D = 8 * lph;
   const int hs = lane / lph, j = lane - hs * lph;
   const bool live = hs < hpw;
-  const int half = a.D >> 1;
+  const int half = D >> 1;
   const uint32_t tasks = uint32_t(a.n_tokens) * uint32_t(a.chunks);
   const uint32_t warps = gridDim.x * (blockDim.x >> 5);
   st::pdl_trigger();
   st::pdl_wait();
   const T *q = static_cast<const T *>(st::after_wait(a.q)), *k = static_cast<const T *>(st::after_wait(a.k));
-  const float *gq = st::after_wait(a.gq), *gk = st::after_wait(a.gk);
   const float4 *table = st::after_wait(a.table);
   const int *positions = st::after_wait(a.positions);
-  // the lane's gains of Q and of K
-  float gains[2][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int d = HALVES ? (i < 4 ? 4 * j + i : half + 4 * j + i - 4) : 8 * j + i;
-    gains[0][i] = gq && live ? gq[d] : 1.f;
-    gains[1][i] = gk && live ? gk[d] : 1.f;
+  if (int(threadIdx.x) < D) {
+    const float *gq = st::after_wait(a.gq), *gk = st::after_wait(a.gk);
+    gains[0][threadIdx.x] = gq ? gq[threadIdx.x] : 1.f;
+    gains[1][threadIdx.x] = gk ? gk[threadIdx.x] : 1.f;
   }
-  const float inv_d = 1.f / float(a.D);
-  for (uint32_t t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); t < tasks; t += warps) {
-    const uint32_t token = st::fdiv(t, a.dchunk);
-    int c = int(t - token * uint32_t(a.chunks));
-    const bool is_k = c >= a.chunks_q;
-    if (is_k) c -= a.chunks_q;
-    const int H = is_k ? a.hk : a.hq;
-    const T *src = is_k ? k + (long long)token * a.sk : q + (long long)token * a.sq;
-    T *dst = is_k ? static_cast<T *>(a.ko) + (long long)token * a.sko : static_cast<T *>(a.qo) + (long long)token * a.sqo;
-    const int h0 = c * UNROLL * hpw + hs;
+  __syncthreads();
+  const float inv_d = 1.f / float(D);
+  const int d0 = HALVES ? 4 * j : 8 * j, d1 = HALVES ? half + 4 * j : 8 * j + 4;
+
+  struct Task {
+    uint32_t token;
+    int h0, pos;               // the lane's first head, the token's row of the table
+  };
+  Lane8<T, HALVES> next[UNROLL];
+  auto fetch = [&](uint32_t t, Task &task) {
+    task.token = st::fdiv(t, a.dchunk);
+    task.h0 = int(t - task.token * uint32_t(a.chunks)) * UNROLL * hpw + hs;
+    const T *rq = q + (long long)task.token * a.sq, *rk = k + (long long)task.token * a.sk - a.hq * D;
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int h = task.h0 + u * hpw;
+      if (live && h < a.heads) next[u].load((h < a.hq ? rq : rk) + h * D, j, half);
+    }
+    if constexpr (ROPE) {
+      if (positions) task.pos = positions[task.token];
+      else task.pos = int(task.token - st::fdiv(task.token, a.dperiod) * uint32_t(a.period));
+    }
+  };
+  uint32_t t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  Task task;
+  if (t < tasks) fetch(t, task);
+  for (; t < tasks; t += warps) {
+    const Task cur = task;
     Lane8<T, HALVES> v[UNROLL];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
-      if (live && h0 + u * hpw < H) v[u].load(src + (long long)(h0 + u * hpw) * a.D, j, half);
+    for (int u = 0; u < UNROLL; ++u) v[u] = next[u];
     float4 cs0 = make_float4(1.f, 0.f, 1.f, 0.f), cs1 = cs0;
     if constexpr (ROPE) {
-      const int pos = positions ? positions[token] : int(token - st::fdiv(token, a.dperiod) * uint32_t(a.period));
-      if (pos >= 0 && pos < a.n_pos && live) {   // a position outside the table turns nothing
-        const float4 *row = table + (long long)pos * (a.D >> 2) + 2 * j;
+      if (cur.pos >= 0 && cur.pos < a.n_pos && live) {       // a position outside the table turns nothing
+        const float4 *row = table + (long long)cur.pos * (D >> 2) + 2 * j;
         cs0 = row[0];
         cs1 = row[1];
       }
     }
+    if (t + warps < tasks) fetch(t + warps, task);
+    float ss[UNROLL];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-      const int h = h0 + u * hpw;
-      if (c * UNROLL * hpw + u * hpw >= H) break;   // the same for the whole warp
-      const bool on = live && h < H;
-      float x[8];
-      float ss = 0.f;
-      if (on) {
-        v[u].get(x);
+      f32x2 x[4];
+      v[u].get(x);             // (lanes past the heads: registers of no row, whose sums no one uses)
+      f32x2 s = fmul2(x[0], x[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-      }
-      // sum over the lph lanes of the head, in the order of a fixed tree
-      for (int o = 1; o < lph; o <<= 1) {
-        const float y = __shfl_down_sync(0xffffffffu, ss, o);
-        if (j + o < lph) ss += y;
-      }
-      ss = __shfl_sync(0xffffffffu, ss, (hs < hpw ? hs : 0) * lph);
-      if (!on) continue;
-      const float inv = 1.f / sqrtf(fmaf(ss, inv_d, a.eps));
+      for (int i = 1; i < 4; ++i) s = ffma2(x[i], x[i], s);
+      ss[u] = unpair(s).x + unpair(s).y;
+    }
+    // sums over the lanes of a head, in the order of a fixed tree
+    if constexpr (LPH != 0 && (LPH & (LPH - 1)) == 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * (is_k ? gains[1][i] : gains[0][i]);
-      if constexpr (ROPE) {
-        const float co[4] = {cs0.x, cs0.z, cs1.x, cs1.z}, si[4] = {cs0.y, cs0.w, cs1.y, cs1.w};
+      for (int o = 1; o < LPH; o <<= 1)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float &p0 = HALVES ? x[i] : x[2 * i], &p1 = HALVES ? x[4 + i] : x[2 * i + 1];
-          const float y0 = p0 * co[i] - p1 * si[i];
-          p1 = p0 * si[i] + p1 * co[i];
-          p0 = y0;
+        for (int u = 0; u < UNROLL; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
+    } else {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        if (o >= lph) break;
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+          const float y = __shfl_down_sync(0xffffffffu, ss[u], o);
+          if (j + o < lph) ss[u] += y;
         }
       }
-      Lane8<T, HALVES>::store(dst + (long long)h * a.D, j, half, x);
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) ss[u] = __shfl_sync(0xffffffffu, ss[u], (live ? hs : 0) * lph);
+    }
+    f32x2 co[2], si[2], nsi[2];
+    if constexpr (ROPE && HALVES) {
+      co[0] = pair(cs0.x, cs0.z);
+      co[1] = pair(cs1.x, cs1.z);
+      si[0] = pair(cs0.y, cs0.w);
+      si[1] = pair(cs1.y, cs1.w);
+      nsi[0] = pair(-cs0.y, -cs0.w);
+      nsi[1] = pair(-cs1.y, -cs1.w);
+    }
+    T *wq = static_cast<T *>(a.qo) + (long long)cur.token * a.sqo, *wk = static_cast<T *>(a.ko) + (long long)cur.token * a.sko - a.hq * D;
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int h = cur.h0 + u * hpw;
+      if (!live || h >= a.heads) continue;
+      f32x2 x[4];              // the lane's channels d0 .. d0 + 3, d1 .. d1 + 3
+      v[u].get(x);
+      const float inv = inv_sqrt(fmaf(ss[u], inv_d, a.eps));
+      const float *g = gains[h < a.hq ? 0 : 1];
+      const ulonglong2 g0 = *reinterpret_cast<const ulonglong2 *>(g + d0), g1 = *reinterpret_cast<const ulonglong2 *>(g + d1);
+      const f32x2 gx[4] = {g0.x, g0.y, g1.x, g1.y}, inv2 = pair(inv, inv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = fmul2(fmul2(x[i], inv2), gx[i]);
+      if constexpr (ROPE && HALVES) {          // (x[0], x[1]) with (x[2], x[3])
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const f32x2 p0 = x[i], p1 = x[2 + i];
+          x[i] = ffma2(p1, nsi[i], fmul2(p0, co[i]));
+          x[2 + i] = ffma2(p0, si[i], fmul2(p1, co[i]));
+        }
+      } else if constexpr (ROPE) {             // the two of each pair
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 p = unpair(x[i]);
+          const float4 cs = i < 2 ? cs0 : cs1;
+          const float c = i & 1 ? cs.z : cs.x, sn = i & 1 ? cs.w : cs.y;
+          x[i] = ffma2(pair(p.y, p.x), pair(-sn, sn), fmul2(x[i], pair(c, c)));
+        }
+      }
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[2 * i] = unpair(x[i]).x;
+        y[2 * i + 1] = unpair(x[i]).y;
+      }
+      Lane8<T, HALVES>::store((h < a.hq ? wq : wk) + h * D, j, half, y);
     }
   }
 }
 
-template <typename T> st_status launch(const QkArgs &a, int pairing, cudaStream_t s) {
+template <typename T, bool HALVES, bool ROPE, int UNROLL> st_status launch_groups(const QkArgs &a, cudaStream_t s) {
   const long long tasks = (long long)a.n_tokens * a.chunks;
-  const long long want = (tasks + 7) / 8, cap = (long long)st::num_sms() * 8;
-  const int grid = int(want < cap ? want : cap);
-  if (a.table)
-    return pairing == ST_ROPE_HALVES ? st::launch_pdl(qk_norm_rope<T, true, true>, grid, 256, 0, s, a)
-                                     : st::launch_pdl(qk_norm_rope<T, false, true>, grid, 256, 0, s, a);
-  return st::launch_pdl(qk_norm_rope<T, false, false>, grid, 256, 0, s, a);
+  const long long want = (tasks + 7) / 8, cap = (long long)st::num_sms() * 3;
+  const dim3 grid(unsigned(want < cap ? want : cap));
+  switch (a.D) {
+    case 32: return st::launch_pdl(qk_norm_rope<T, HALVES, ROPE, 4, UNROLL>, grid, 256, 0, s, a);
+    case 64: return st::launch_pdl(qk_norm_rope<T, HALVES, ROPE, 8, UNROLL>, grid, 256, 0, s, a);
+    case 72: return st::launch_pdl(qk_norm_rope<T, HALVES, ROPE, 9, UNROLL>, grid, 256, 0, s, a);
+    case 80: return st::launch_pdl(qk_norm_rope<T, HALVES, ROPE, 10, UNROLL>, grid, 256, 0, s, a);
+    case 96: return st::launch_pdl(qk_norm_rope<T, HALVES, ROPE, 12, UNROLL>, grid, 256, 0, s, a);
+    case 128: return st::launch_pdl(qk_norm_rope<T, HALVES, ROPE, 16, UNROLL>, grid, 256, 0, s, a);
+    default: return st::launch_pdl(qk_norm_rope<T, HALVES, ROPE, 0, UNROLL>, grid, 256, 0, s, a);
+  }
+}
+// Four groups of bf16 a task, or three where that leaves fewer places empty
+// (48 heads of 128 channels: 289 us with four, 309 with three; 20 heads of 64,
+// five groups: 77 and 67); two of fp32 (four spill).
+template <typename T, bool HALVES, bool ROPE> st_status launch_pairing(QkArgs a, cudaStream_t s) {
+  const int hpw = 32 / (a.D / 8), groups = (a.heads + hpw - 1) / hpw;
+  const bool three = (groups + 2) / 3 * 3 < (groups + 3) / 4 * 4;
+  const int unroll = sizeof(T) == 4 ? 2 : (three ? 3 : 4);
+  a.chunks = (groups + unroll - 1) / unroll;
+  if ((long long)a.n_tokens * a.chunks >= (1LL << 31) - (1LL << 24)) return ST_ERR_SHAPE;
+  a.dchunk = st::make_fastdiv(uint32_t(a.chunks));
+  if constexpr (sizeof(T) == 4) return launch_groups<T, HALVES, ROPE, 2>(a, s);
+  else return three ? launch_groups<T, HALVES, ROPE, 3>(a, s) : launch_groups<T, HALVES, ROPE, 4>(a, s);
+}
+template <typename T> st_status launch(const QkArgs &a, int pairing, cudaStream_t s) {
+  if (!a.table) return launch_pairing<T, false, false>(a, s);
+  return pairing == ST_ROPE_HALVES ? launch_pairing<T, true, true>(a, s) : launch_pairing<T, false, true>(a, s);
 }
 
 struct Rows {
@@ -242,14 +346,9 @@ ST_API st_status st_qk_norm_rope(const st_qk_desc *d, const void *q, const void 
   a.period = d->pos_period ? d->pos_period : d->n_tokens;
   a.n_tokens = d->n_tokens;
   a.hq = d->h_q;
-  a.hk = d->h_k;
+  a.heads = d->h_q + d->h_k;
   a.D = d->D;
   a.eps = d->eps;
-  const int heads = 32 / (d->D / 8) * UNROLL;  // heads of a task
-  a.chunks_q = (d->h_q + heads - 1) / heads;
-  a.chunks = a.chunks_q + (d->h_k + heads - 1) / heads;
-  if ((long long)a.n_tokens * a.chunks >= (1LL << 31) - (1LL << 24)) return ST_ERR_SHAPE;
-  a.dchunk = st::make_fastdiv(uint32_t(a.chunks));
   a.dperiod = st::make_fastdiv(uint32_t(a.period));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return d->dtype == ST_BF16 ? launch<uint16_t>(a, d->pairing, s) : launch<float>(a, d->pairing, s);
