@@ -361,41 +361,43 @@ def _device_call(where, fn, device, stream, *args):
         return fn(*args, _stream(stream))
 
 
-def _expect(ok, code, what):
-    if not ok:
-        raise StattnError(code, what)
-
-
-def _same_device(where, device, *tensors):
+# The checks below run on every call and build their messages only when they fail.
+def _same_device(where, index, *tensors):
     for t in tensors:
-        _expect(t is None or t.device == device, ST_ERR_SHAPE, f"{where}: tensors on different devices")
+        if t is not None and t.get_device() != index:
+            raise StattnError(ST_ERR_SHAPE, f"{where}: tensors on different devices")
 
 
-def _int32(where, t, n, device):
+def _int32(where, t, n, index):
     """Pointer of an optional contiguous int32 tensor of n elements."""
     if t is None:
         return None
     import torch
-    _expect(t.dtype == torch.int32, ST_ERR_DTYPE, f"{where}: lengths, offsets and positions are int32")
-    _expect(t.numel() == n and t.is_contiguous() and t.device == device, ST_ERR_SHAPE,
-            f"{where}: {n} contiguous int32 on the tensors' device expected")
+    if t.dtype != torch.int32:
+        raise StattnError(ST_ERR_DTYPE, f"{where}: lengths, offsets and positions are int32")
+    if t.numel() != n or not t.is_contiguous() or t.get_device() != index:
+        raise StattnError(ST_ERR_SHAPE, f"{where}: {n} contiguous int32 on the tensors' device expected")
     return t.data_ptr()
 
 
 def _rows(where, t):
     """(tokens, H, D, elements between tokens) of a [..., H, D] tensor whose tokens have one stride."""
-    _expect(t.dim() >= 3, ST_ERR_SHAPE, f"{where}: [..., H, D] expected")
     size, stride = t.shape, t.stride()
+    if len(size) < 3:
+        raise StattnError(ST_ERR_SHAPE, f"{where}: [..., H, D] expected")
     H, D = size[-2], size[-1]
-    _expect((D == 1 or stride[-1] == 1) and (H == 1 or stride[-2] == D), ST_ERR_SHAPE, f"{where}: heads must be dense")
+    if (D != 1 and stride[-1] != 1) or (H != 1 and stride[-2] != D):
+        raise StattnError(ST_ERR_SHAPE, f"{where}: heads must be dense")
     n, step = 1, 0
     for i in range(len(size) - 3, -1, -1):
         if size[i] == 1:
             continue
-        _expect(n == 1 or stride[i] == n * step, ST_ERR_SHAPE, f"{where}: tokens must have one stride")
         if n == 1:
             step = stride[i]
-            _expect(step > 0, ST_ERR_SHAPE, f"{where}: expanded tensors are not taken")
+            if step <= 0:
+                raise StattnError(ST_ERR_SHAPE, f"{where}: expanded tensors are not taken")
+        elif stride[i] != n * step:
+            raise StattnError(ST_ERR_SHAPE, f"{where}: tokens must have one stride")
         n *= size[i]
     return n, H, D, step
 
@@ -407,54 +409,65 @@ def st_qk_norm_rope(q, k=None, q_out=None, k_out=None, q_gamma=None, k_gamma=Non
     q, k: [..., H, D] with one stride between tokens (views of a fused projection
     included); either may be None.  Outputs default to in place."""
     import torch
+    where = "st_qk_norm_rope"
     x = q if q is not None else k
-    _expect(x is not None, ST_ERR_NULL, "st_qk_norm_rope: q or k")
+    if x is None:
+        raise StattnError(ST_ERR_NULL, f"{where}: q or k")
     d = st_qk_desc(size=ctypes.sizeof(st_qk_desc), dtype=_dtype_code(x), eps=float(eps), pos_period=int(pos_period),
                    pairing=PAIRINGS[pairing] if isinstance(pairing, str) else int(pairing))
+    index, dtype = x.get_device(), x.dtype
+    tokens = head_dim = None
     for name, t, out, gamma in (("q", q, q_out, q_gamma), ("k", k, k_out, k_gamma)):
         if t is None:
-            _expect(out is None, ST_ERR_NULL, f"st_qk_norm_rope: {name}_out without {name}")
+            if out is not None:
+                raise StattnError(ST_ERR_NULL, f"{where}: {name}_out without {name}")
             continue
-        n, H, D, step = _rows("st_qk_norm_rope", t)
-        _expect(d.n_tokens in (0, n) and d.D in (0, D), ST_ERR_SHAPE, "st_qk_norm_rope: q and k differ in tokens or D")
-        d.n_tokens, d.D = n, D
-        setattr(d, "h_" + name, H)
-        setattr(d, "stride_" + name, step)
+        n, H, D, step = _rows(where, t)
+        if tokens is not None and (n != tokens or D != head_dim):
+            raise StattnError(ST_ERR_SHAPE, f"{where}: q and k differ in tokens or D")
+        tokens, head_dim, out_step = n, D, step
         if out is not None:
-            _expect(out.shape == t.shape, ST_ERR_SHAPE, f"st_qk_norm_rope: {name}_out has another shape")
-            step = _rows("st_qk_norm_rope", out)[3]
-        setattr(d, f"stride_{name}_out", step)
-        _same_device("st_qk_norm_rope", x.device, t, out, gamma)
-        _expect(t.dtype == x.dtype and (out is None or out.dtype == x.dtype), ST_ERR_DTYPE,
-                "st_qk_norm_rope: one dtype for q, k and the outputs")
-        _expect(gamma is None or (gamma.dtype == torch.float32 and gamma.numel() == D and gamma.is_contiguous()),
-                ST_ERR_SHAPE, f"st_qk_norm_rope: {name}_gamma is fp32 [D]")
+            if out.shape != t.shape:
+                raise StattnError(ST_ERR_SHAPE, f"{where}: {name}_out has another shape")
+            out_step = _rows(where, out)[3]
+        if name == "q":
+            d.h_q, d.stride_q, d.stride_q_out = H, step, out_step
+        else:
+            d.h_k, d.stride_k, d.stride_k_out = H, step, out_step
+        _same_device(where, index, t, out, gamma)
+        if t.dtype != dtype or (out is not None and out.dtype != dtype):
+            raise StattnError(ST_ERR_DTYPE, f"{where}: one dtype for q, k and the outputs")
+        if gamma is not None and (gamma.dtype != torch.float32 or gamma.numel() != D or not gamma.is_contiguous()):
+            raise StattnError(ST_ERR_SHAPE, f"{where}: {name}_gamma is fp32 [D]")
+    d.n_tokens, d.D = tokens, head_dim
     n_pos = 0
     if rope_table is not None:
-        _same_device("st_qk_norm_rope", x.device, rope_table)
+        _same_device(where, index, rope_table)
         n_pos = rope_table.shape[0]
-        _expect(rope_table.dtype == torch.float32 and rope_table.is_contiguous() and
-                rope_table.numel() == n_pos * d.D, ST_ERR_SHAPE, "st_qk_norm_rope: rope_table is fp32 [n, D / 2, 2]")
-    pos = _int32("st_qk_norm_rope", positions, d.n_tokens, x.device)
-    r = _device_call("st_qk_norm_rope", _c["st_qk_norm_rope"], x.device, stream, ctypes.byref(d), _ptr(q), _ptr(k),
+        if rope_table.dtype != torch.float32 or not rope_table.is_contiguous() or rope_table.numel() != n_pos * head_dim:
+            raise StattnError(ST_ERR_SHAPE, f"{where}: rope_table is fp32 [n, D / 2, 2]")
+    pos = _int32(where, positions, tokens, index)
+    r = _device_call(where, _c["st_qk_norm_rope"], x.device, stream, ctypes.byref(d), _ptr(q), _ptr(k),
                      _ptr(q if q_out is None else q_out), _ptr(k if k_out is None else k_out), _ptr(q_gamma),
                      _ptr(k_gamma), _ptr(rope_table), n_pos, pos)
-    return r if raw else _check(r, "st_qk_norm_rope")
+    return r if raw else _check(r, where)
 
 
 def _q_desc(where, q, o, kw):
     """Descriptor of Q and O [B, T, S, H, D], strides taken from the tensors."""
-    _expect(q.dim() == 5, ST_ERR_SHAPE, f"{where}: q is [B, T, S, H, D]")
-    B, T, S, H, D = q.shape
-    for t in (q, o):
-        if t is None:
-            continue
-        st = t.stride()
-        _expect(t.shape == q.shape and (D == 1 or st[4] == 1) and (H == 1 or st[3] == D), ST_ERR_SHAPE,
-                f"{where}: q and o are [B, T, S, H, D] with dense heads")
-        _expect(all(n == 1 or (a > 0 and a == b) for n, a, b in zip(q.shape[:3], st, q.stride())), ST_ERR_SHAPE,
-                f"{where}: q and o need the same strides")
-    sb, ss, stt = (q.stride(i) if q.shape[i] > 1 else 0 for i in (0, 2, 1))
+    size, st = q.shape, q.stride()
+    if len(size) != 5:
+        raise StattnError(ST_ERR_SHAPE, f"{where}: q is [B, T, S, H, D]")
+    B, T, S, H, D = size
+    if (D != 1 and st[4] != 1) or (H != 1 and st[3] != D) or (o is not None and o.shape != size):
+        raise StattnError(ST_ERR_SHAPE, f"{where}: q and o are [B, T, S, H, D] with dense heads")
+    so = st if o is None else o.stride()
+    if so != st and ((D != 1 and so[4] != 1) or (H != 1 and so[3] != D)):
+        raise StattnError(ST_ERR_SHAPE, f"{where}: q and o are [B, T, S, H, D] with dense heads")
+    for i in range(3):
+        if size[i] != 1 and (st[i] <= 0 or so[i] != st[i]):
+            raise StattnError(ST_ERR_SHAPE, f"{where}: q and o need the same strides")
+    sb, stt, ss = (st[i] if size[i] > 1 else 0 for i in range(3))
     if T > 1 and stt == S * (ss or H * D):
         stt = 0                                 # dense frames
     return make_desc(B, T, S, H, D, _dtype_code(q), stride_b=sb, stride_t=stt, stride_s=ss, **kw)
@@ -462,56 +475,67 @@ def _q_desc(where, q, o, kw):
 
 def _kv_desc(where, head_dim, q, k, v, length, offsets, mask, max_len):
     """st_kv_desc of K (and V) [n_sets, L, H_kv, D], or packed [rows, H_kv, D] with offsets."""
-    import torch
     packed = offsets is not None
-    _expect(k.dim() == (3 if packed else 4), ST_ERR_SHAPE,
-            f"{where}: keys are [n_sets, L, H_kv, D], or [rows, H_kv, D] with offsets")
-    H, D = k.shape[-2:]
-    L = k.shape[-3]
-    st = k.stride()
-    _expect(D == head_dim and (D == 1 or st[-1] == 1) and (H == 1 or st[-2] == D), ST_ERR_SHAPE,
-            f"{where}: keys need q's head dim and dense heads")
-    _expect(k.dtype == q.dtype and (v is None or v.dtype == q.dtype), ST_ERR_DTYPE, f"{where}: one dtype for q, k and v")
+    size, st = k.shape, k.stride()
+    if len(size) != (3 if packed else 4):
+        raise StattnError(ST_ERR_SHAPE, f"{where}: keys are [n_sets, L, H_kv, D], or [rows, H_kv, D] with offsets")
+    L, H, D = size[-3:]
+    if D != head_dim or (D != 1 and st[-1] != 1) or (H != 1 and st[-2] != D):
+        raise StattnError(ST_ERR_SHAPE, f"{where}: keys need q's head dim and dense heads")
+    if k.dtype != q.dtype or (v is not None and v.dtype != k.dtype):
+        raise StattnError(ST_ERR_DTYPE, f"{where}: one dtype for q, k and v")
     if v is not None:
-        _expect(v.shape == k.shape and all(n == 1 or a == b for n, a, b in zip(k.shape, st, v.stride())),
-                ST_ERR_SHAPE, f"{where}: k and v need the same shape and strides")
-    _same_device(where, q.device, k, v, length, offsets, mask)
-    _expect(L <= 1 or st[-3] > 0, ST_ERR_SHAPE, f"{where}: expanded tensors are not taken")
-    sl = st[-3] if L > 1 else 0
-    d = st_kv_desc(size=ctypes.sizeof(st_kv_desc), L=L, H_kv=H, stride_l=sl)
+        sv = v.stride()
+        if v.shape != size or (sv != st and any(n != 1 and a != b for n, a, b in zip(size, st, sv))):
+            raise StattnError(ST_ERR_SHAPE, f"{where}: k and v need the same shape and strides")
+    index = q.get_device()
+    _same_device(where, index, k, v, length, offsets, mask)
+    if L > 1 and st[-3] <= 0:
+        raise StattnError(ST_ERR_SHAPE, f"{where}: expanded tensors are not taken")
+    d = st_kv_desc(size=ctypes.sizeof(st_kv_desc), L=L, H_kv=H, stride_l=st[-3] if L > 1 else 0)
     if packed:
-        _expect(length is None and mask is None, ST_ERR_SHAPE, f"{where}: offsets exclude lengths and mask")
+        if length is not None or mask is not None:
+            raise StattnError(ST_ERR_SHAPE, f"{where}: offsets exclude lengths and mask")
         d.n_sets, d.n_rows = offsets.numel() - 1, L
-        d.L = int(max_len) if max_len is not None else L
-        d.offsets = _int32(where, offsets, d.n_sets + 1, q.device)
-    else:
-        d.n_sets = k.shape[0]
-        if d.n_sets > 1:
-            _expect(st[0] > 0, ST_ERR_SHAPE, f"{where}: expanded tensors are not taken")
-            d.stride_set = st[0]
-        d.len = _int32(where, length, d.n_sets, q.device)
-        if mask is not None:
-            _expect(mask.dtype in (torch.uint8, torch.bool), ST_ERR_DTYPE, f"{where}: the mask is uint8 or bool")
-            _expect(mask.shape == k.shape[:2] and mask.is_contiguous(), ST_ERR_SHAPE, f"{where}: the mask is [n_sets, L]")
-            d.mask = mask.data_ptr()
+        if max_len is not None:
+            d.L = int(max_len)
+        d.offsets = _int32(where, offsets, d.n_sets + 1, index)
+        return d
+    n = size[0]
+    d.n_sets = n
+    if n > 1:
+        if st[0] <= 0:
+            raise StattnError(ST_ERR_SHAPE, f"{where}: expanded tensors are not taken")
+        d.stride_set = st[0]
+    if length is not None:
+        d.len = _int32(where, length, n, index)
+    if mask is not None:
+        import torch
+        if mask.dtype not in (torch.uint8, torch.bool):
+            raise StattnError(ST_ERR_DTYPE, f"{where}: the mask is uint8 or bool")
+        if mask.shape != size[:2] or not mask.is_contiguous():
+            raise StattnError(ST_ERR_SHAPE, f"{where}: the mask is [n_sets, L]")
+        d.mask = mask.data_ptr()
     return d
 
 
 def _workspace(where, t, device):
     if t is None or t.numel() == 0:
         return None, 0
-    _expect(t.device == device and t.is_contiguous(), ST_ERR_SHAPE, f"{where}: workspace")
+    if t.device != device or not t.is_contiguous():
+        raise StattnError(ST_ERR_SHAPE, f"{where}: workspace")
     return _ptr(t), t.numel() * t.element_size()
 
 
 def _check_out(where, q, o, lse, o_fp32):
     import torch
-    _expect(o.dtype == (torch.float32 if o_fp32 else q.dtype), ST_ERR_DTYPE, f"{where}: o's dtype")
-    _same_device(where, q.device, o, lse)
+    if o.dtype != (torch.float32 if o_fp32 else q.dtype):
+        raise StattnError(ST_ERR_DTYPE, f"{where}: o's dtype")
+    _same_device(where, q.get_device(), o, lse)
     if lse is not None:
         B, T, S, H, _ = q.shape
-        _expect(lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == B * T * H * S, ST_ERR_SHAPE,
-                f"{where}: lse is fp32 [B, T, H, S]")
+        if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.numel() != B * T * H * S:
+            raise StattnError(ST_ERR_SHAPE, f"{where}: lse is fp32 [B, T, H, S]")
 
 
 def st_attn_cross(q, k, v, o, lse=None, *, kv_len=None, kv_offsets=None, kv_mask=None, max_len=None, workspace=None,
