@@ -93,7 +93,7 @@ __device__ __forceinline__ long long cond_lse(const CondParams &p, int unit, int
 // SMs of the current device, whatever the thread's budget.
 int device_sms();
 
-st_status cond_simt(const CondParams &p, st_dtype dtype, cudaStream_t s);
+st_status cond_simt(const CondParams &p, cudaStream_t s);
 // What a kernel walks: rows of a tile, tiles of a work item, keys per step.
 struct CondTile {
   int rows, tiles, keys;

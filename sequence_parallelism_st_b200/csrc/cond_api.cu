@@ -394,7 +394,7 @@ st_status run(const st_attn_desc *desc, const st_kv_desc *d0, const st_kv_desc *
     p.part_lse = p.part_o + (long long)p.n_split * p.part_rows * p.g.D;
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  s = bf16 ? st::cond_sm100(p, st) : st::cond_simt(p, pl.dtype, st);
+  s = bf16 ? st::cond_sm100(p, st) : st::cond_simt(p, st);
   if (s != ST_OK || !pl.workspace) return s;
   return bf16 ? combine<uint16_t>(p, st) : combine<float>(p, st);
 }

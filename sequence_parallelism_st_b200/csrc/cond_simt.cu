@@ -16,44 +16,36 @@ namespace {
 
 constexpr int BM = 64, BN = 64, NT = 256;
 
-template <typename T> __device__ __forceinline__ float4 load4(const T *p);
-template <> __device__ __forceinline__ float4 load4<float>(const float *p) {
-  return make_float4(p[0], p[1], p[2], p[3]);
-}
-template <> __device__ __forceinline__ float4 load4<uint16_t>(const uint16_t *p) {
-  return make_float4(st::bf16_to_f32(p[0]), st::bf16_to_f32(p[1]), st::bf16_to_f32(p[2]), st::bf16_to_f32(p[3]));
+// Channels c .. c + 3 of a row (n of them exist); rows of 16-byte vectors where
+// the head dim, the strides and the pointers allow.
+__device__ __forceinline__ float4 load4(const float *p, int n, bool vec) {
+  if (vec) return *reinterpret_cast<const float4 *>(p);
+  return make_float4(p[0], n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
 }
 
 // NC: 64-channel chunks of the head (D <= 64 * NC)
-template <typename T, int NC>
-__global__ void __launch_bounds__(NT) cond_simt_kernel(const __grid_constant__ st::CondParams p, int row_blocks) {
+template <int NC>
+__global__ void __launch_bounds__(NT) cond_simt_kernel(const __grid_constant__ st::CondParams p, uint32_t row_blocks, bool vec) {
   extern __shared__ float sm[];
   const int D = p.g.D, DP = (D + 3) / 4 * 4, PQ = DP + 4;
   float *sQ = sm, *sK = sQ + BM * PQ, *sV = sK + (BM * (PQ > BN + 4 ? PQ : BN + 4));
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  long long x = blockIdx.x;
+  uint32_t x = blockIdx.x;
   const int rb = int(x % row_blocks);
   x /= row_blocks;
-  const int sp = int(x % p.n_split);
-  x /= p.n_split;
-  const int w = int(x % p.HW), unit = int(x / p.HW);
+  const int sp = int(x % uint32_t(p.n_split));
+  x /= uint32_t(p.n_split);
+  const int w = int(x % uint32_t(p.HW)), unit = int(x / uint32_t(p.HW));
   const int rows = p.R, r0 = rb * BM;
   const int kvh = w / p.hdiv;
-  const T *Q = static_cast<const T *>(p.q);
-  for (int i = tid; i < BM * (DP / 4); i += NT) {
-    const int r = i / (DP / 4), c = (i - r * (DP / 4)) * 4;
+  st::pdl_trigger();
+  st::pdl_wait();
+  const float *Q = static_cast<const float *>(st::after_wait(p.q));
+  const int vpr = DP / 4;                      // vectors of a row
+  for (int i = tid; i < BM * vpr; i += NT) {
+    const int r = i / vpr, c = (i - r * vpr) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r0 + r < rows) {
-      const T *src = Q + st::cond_row(p, unit, w, r0 + r) + c;
-      if (c + 4 <= D) v = load4(src);
-      else {
-        float *e = &v.x;
-        for (int d = 0; c + d < D; ++d) {
-          if constexpr (sizeof(T) == 2) e[d] = st::bf16_to_f32(src[d]);
-          else e[d] = src[d];
-        }
-      }
-    }
+    if (r0 + r < rows) v = load4(Q + st::cond_row(p, unit, w, r0 + r) + c, D - c, vec);
     *reinterpret_cast<float4 *>(sQ + r * PQ + c) = v;
   }
   float m[4], l[4], acc[4][NC][4];
@@ -70,7 +62,10 @@ __global__ void __launch_bounds__(NT) cond_simt_kernel(const __grid_constant__ s
   st::KvRange kr[2];
   int steps[2] = {0, 0};
   for (int g = 0; g < p.n_seg; ++g) {
-    kr[g] = st::kv_range(p.seg[g], st::cond_batch(p, unit));
+    st::KvSeg sg = p.seg[g];
+    sg.len = st::after_wait(sg.len);
+    sg.offsets = st::after_wait(sg.offsets);
+    kr[g] = st::kv_range(sg, st::cond_batch(p, unit));
     steps[g] = (kr[g].n + BN - 1) / BN;
   }
   const long long total = (long long)steps[0] + steps[1];
@@ -82,30 +77,18 @@ __global__ void __launch_bounds__(NT) cond_simt_kernel(const __grid_constant__ s
     const int nv = min(BN, kr[g].n - key0);
     const long long base = (long long)kr[g].set * (sg.offsets ? 0 : sg.stride_set) +
                            (long long)(kr[g].row0 + key0) * sg.stride_l + (long long)kvh * D;
-    const T *Kp = static_cast<const T *>(sg.k) + base, *Vp = static_cast<const T *>(sg.v) + base;
-    const unsigned char *mk = sg.mask ? sg.mask + (long long)kr[g].set * sg.L + key0 : nullptr;
+    const float *Kp = static_cast<const float *>(st::after_wait(sg.k)) + base;
+    const float *Vp = static_cast<const float *>(st::after_wait(sg.v)) + base;
+    const unsigned char *mk = sg.mask ? st::after_wait(sg.mask) + (long long)kr[g].set * sg.L + key0 : nullptr;
     __syncthreads();
-    for (int i = tid; i < BN * (DP / 4); i += NT) {
-      const int r = i / (DP / 4), c = (i - r * (DP / 4)) * 4;
+    for (int i = tid; i < BN * vpr; i += NT) {
+      const int r = i / vpr, c = (i - r * vpr) * 4;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
       // a key that does not count is never read, so its V cannot reach the sum
       if (r < nv && (!mk || mk[r])) {
         const long long off = (long long)r * sg.stride_l + c;
-        if (c + 4 <= D) {
-          a = load4(Kp + off);
-          b = load4(Vp + off);
-        } else {
-          float *ea = &a.x, *eb = &b.x;
-          for (int d = 0; c + d < D; ++d) {
-            if constexpr (sizeof(T) == 2) {
-              ea[d] = st::bf16_to_f32(Kp[off + d]);
-              eb[d] = st::bf16_to_f32(Vp[off + d]);
-            } else {
-              ea[d] = Kp[off + d];
-              eb[d] = Vp[off + d];
-            }
-          }
-        }
+        a = load4(Kp + off, D - c, vec);
+        b = load4(Vp + off, D - c, vec);
       }
       *reinterpret_cast<float4 *>(sK + r * PQ + c) = a;
       *reinterpret_cast<float4 *>(sV + r * DP + c) = b;
@@ -121,16 +104,19 @@ __global__ void __launch_bounds__(NT) cond_simt_kernel(const __grid_constant__ s
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(sQ + (4 * ty + i) * PQ + d);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * e) * PQ + d);
+      for (int e = 0; e < 4; ++e)
+        if (16 * e < nv) b[e] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * e) * PQ + d);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int e = 0; e < 4; ++e) {
+        if (16 * e >= nv) break;               // no key of the tile's there: uniform
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int i = 0; i < 4; ++i) {
           s[i][e] = fmaf(a[i].x, b[e].x, s[i][e]);
           s[i][e] = fmaf(a[i].y, b[e].y, s[i][e]);
           s[i][e] = fmaf(a[i].z, b[e].z, s[i][e]);
           s[i][e] = fmaf(a[i].w, b[e].w, s[i][e]);
         }
+      }
     }
     bool keep[4];
 #pragma unroll
@@ -169,7 +155,7 @@ __global__ void __launch_bounds__(NT) cond_simt_kernel(const __grid_constant__ s
         for (int e = 0; e < 4; ++e) acc[i][c][e] *= corr;
     }
     __syncthreads();
-    for (int k = 0; k < BN; k += 4) {
+    for (int k = 0; k < nv; k += 4) {          // (weights past nv are 0)
       float4 pr[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) pr[i] = *reinterpret_cast<const float4 *>(sK + (4 * ty + i) * (BN + 4) + k);
@@ -209,8 +195,7 @@ __global__ void __launch_bounds__(NT) cond_simt_kernel(const __grid_constant__ s
         if (d >= D) continue;
         const float y = acc[i][c][e] * inv;
         if (p.part_o) p.part_o[off + d] = y;
-        else if (sizeof(T) == 4 || p.o_f32) static_cast<float *>(p.o)[off + d] = y;
-        else static_cast<uint16_t *>(p.o)[off + d] = st::f32_to_bf16(y);
+        else static_cast<float *>(p.o)[off + d] = y;
       }
     if (tx == 0) {
       if (p.part_o) p.part_lse[prow] = lse;
@@ -219,27 +204,30 @@ __global__ void __launch_bounds__(NT) cond_simt_kernel(const __grid_constant__ s
   }
 }
 
-template <typename T, int NC> st_status launch(const st::CondParams &p, cudaStream_t s) {
+template <int NC> st_status launch(const st::CondParams &p, cudaStream_t s) {
   const int DP = (p.g.D + 3) / 4 * 4, PQ = DP + 4;
   const size_t smem = size_t(BM * PQ + BM * (PQ > BN + 4 ? PQ : BN + 4) + BN * DP) * 4;
   const int row_blocks = (p.R + BM - 1) / BM;
   const long long grid = (long long)row_blocks * p.n_split * p.HW * st::cond_units(p);
   if (grid > 0x7fffffffLL) return ST_ERR_SHAPE;
-  auto kern = cond_simt_kernel<T, NC>;
+  const st::Geom &g = p.g;
+  bool vec = g.D % 4 == 0 && st::is_aligned(p.q, 16) && g.ss % 4 == 0 && g.st % 4 == 0 && g.stb % 4 == 0 && g.sb % 4 == 0;
+  for (int i = 0; i < p.n_seg; ++i)
+    vec = vec && st::is_aligned(p.seg[i].k, 16) && st::is_aligned(p.seg[i].v, 16) && p.seg[i].stride_l % 4 == 0 &&
+          p.seg[i].stride_set % 4 == 0;
+  auto kern = cond_simt_kernel<NC>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
     return ST_ERR_CUDA;
-  kern<<<unsigned(grid), NT, smem, s>>>(p, row_blocks);
-  return st::launch_status();
+  return st::launch_pdl(kern, dim3(unsigned(grid)), dim3(NT), smem, s, p, uint32_t(row_blocks), vec);
 }
 
 }  // namespace
 
 namespace st {
 
-st_status cond_simt(const CondParams &p, st_dtype dtype, cudaStream_t s) {
+st_status cond_simt(const CondParams &p, cudaStream_t s) {
   if (p.g.D > 128) return ST_ERR_UNSUPPORTED;
-  if (dtype == ST_F32) return p.g.D <= 64 ? launch<float, 1>(p, s) : launch<float, 2>(p, s);
-  return p.g.D <= 64 ? launch<uint16_t, 1>(p, s) : launch<uint16_t, 2>(p, s);
+  return p.g.D <= 64 ? launch<1>(p, s) : launch<2>(p, s);
 }
 
 }  // namespace st

@@ -446,7 +446,10 @@ __device__ __forceinline__ void set_range(const Args &a, const int2 *table, int 
     row = r.x;
     n = r.y;
   } else {
-    const st::KvRange r = st::kv_range(a.c.seg[g], b);
+    st::KvSeg sg = a.c.seg[g];
+    sg.len = st::after_wait(sg.len);
+    sg.offsets = st::after_wait(sg.offsets);
+    const st::KvRange r = st::kv_range(sg, b);
     row = r.row0;
     n = r.n;
   }
@@ -515,7 +518,8 @@ __device__ __forceinline__ bool same_keys(const Item &a, const Item &b) {
 // at about the same time.  (Heads at different rows at a time: Q and O of
 // 65,536 x 16 heads x 72 ran at 2.3 TB/s.)  Where the sets differ in length
 // the cut is by cost: an item without keys costs about as much as ITEM_STEPS
-// steps.
+// steps.  Finding the cut takes 5 us for 8 units (serial code, read for the
+// first time), so it pays from about four items per CTA on.
 constexpr int ITEM_STEPS = 2, WEIGHED = 16;      // units up to which the cut is by cost
 template <int D> struct Walk {
   int x, end, inc;
@@ -1395,7 +1399,7 @@ template <int D> st_status launch(const st::CondParams &p, cudaStream_t s) {
     a.cols = st::cond_units(p) * p.HW;
     const int share = (a.n_items + ctas - 1) / ctas;
     for (int g = 0; g < p.n_seg; ++g) a.weighed |= p.seg[g].n_sets > 1 && (p.seg[g].len || p.seg[g].offsets);
-    a.weighed = a.weighed && st::cond_units(p) <= WEIGHED;
+    a.weighed = a.weighed && st::cond_units(p) <= WEIGHED && a.n_items >= 4 * ctas;
     const int whole = a.cols <= ctas && !a.weighed ? (a.q_blocks + ctas / a.cols - 1) / (ctas / a.cols) : a.q_blocks + 1;
     a.band = whole <= share ? whole : (share < a.q_blocks ? share : a.q_blocks);
     a.n_bands = (a.q_blocks + a.band - 1) / a.band;
@@ -1419,6 +1423,8 @@ template <int D> st_status launch(const st::CondParams &p, cudaStream_t s) {
   return st::launch_pdl(kern, dim3(ctas), dim3(K::THREADS), K::SMEM, s, m, a);
 }
 
+template <int D> st::CondTile tile_of() { return {BLOCK_M, Cfg<D>::NT, Cfg<D>::BN}; }
+
 }  // namespace
 
 namespace st {
@@ -1436,7 +1442,14 @@ unsigned int read_and_clear_cond_error(cudaStream_t stream, cudaError_t *err) {
 }
 
 CondTile cond_tile(int D) {
-  return D <= 96 ? CondTile{128, 3, D <= 64 ? 96 : (D <= 80 ? 80 : 64)} : CondTile{128, 2, 128};
+  switch (D) {
+    case 32: return tile_of<32>();
+    case 64: return tile_of<64>();
+    case 72: return tile_of<72>();
+    case 80: return tile_of<80>();
+    case 96: return tile_of<96>();
+    default: return tile_of<128>();
+  }
 }
 
 st_status cond_sm100(const CondParams &p, cudaStream_t s) {
