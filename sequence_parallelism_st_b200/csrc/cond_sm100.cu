@@ -1161,7 +1161,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const bool tma = a.tma_out && some;      // (an item without keys has no slot)
       const int row = it.r0 + (spread ? 0 : X * a.tile_rows) + r;   // row of the unit
       const bool valid = r < a.tile_rows && row < a.c.R;
-      const int part = spread ? it.split * NT + X : it.split;
+      const int part = spread ? it.split * NT + first : it.split;   // by its steps, whichever tile took them
       float inv = 0.f, lse = -INFINITY;
       uint8_t *stg = sQ + mine * K::QTILE;
       if (some) {

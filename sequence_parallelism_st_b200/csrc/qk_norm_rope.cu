@@ -38,11 +38,12 @@ __device__ __forceinline__ f32x2 fmul2(f32x2 a, f32x2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// 1 / sqrt(x): the hardware's estimate and one Newton step (x = 0: infinite; NaN stays).
+// 1 / sqrt(x): the hardware's estimate and one Newton step, which 0, infinity and
+// NaN go without.
 __device__ __forceinline__ float inv_sqrt(float x) {
   const float y = rsqrtf(x);
   const float z = fmaf(0.5f * y, fmaf(-x * y, y, 1.f), y);
-  return x > 0.f && y < INFINITY ? z : y;
+  return x > 0.f && x < INFINITY ? z : y;
 }
 
 struct QkArgs {

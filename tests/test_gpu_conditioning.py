@@ -459,3 +459,171 @@ def test_results_do_not_depend_on_the_budget_or_the_run():
         finally:
             st.st_set_sm_budget(0)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,hq,hk,D", [(5001, 20, 20, 64), (9000, 3, 0, 40), (2500, 16, 16, 72), (20000, 1, 1, 256)])
+def test_qk_many_tokens(dtype, n, hq, hk, D):
+    """Every warp walks several tasks: three and four groups of bf16, head dims with and without their own kernel."""
+    q, k = rand(120, n, hq, D, dtype=dtype), rand(121, n, hk, D, dtype=dtype) if hk else None
+    qo, ko = torch.empty_like(q), torch.empty_like(k) if hk else None
+    table = st.st_rope_table(977, D)
+    st.st_qk_norm_rope(q, k, qo, ko, rope_table=table, pos_period=977)
+    pos = np.arange(n) % 977
+    check_qk(qo, q, None, 1e-6, table, pos, "interleaved", "q")
+    if hk:
+        check_qk(ko, k, None, 1e-6, table, pos, "interleaved", "k")
+
+
+def test_qk_offsets_beyond_32_bits():
+    """Tokens 2^31 elements and more apart from the first, in place."""
+    n, step, H, D = 70, 2 ** 25, 2, 72
+    big = torch.empty(n * step, dtype=BF, device="cuda")
+    x = big.as_strided((n, H, D), (step, D, 1))
+    x.copy_(rand(122, n, H, D))
+    before = x.clone()
+    assert (n - 1) * step > 2 ** 31
+    st.st_qk_norm_rope(x, None, eps=1e-5)
+    check_qk(x, before, None, 1e-5, None, None, "interleaved", "q")
+
+
+@pytest.mark.parametrize("budget", [1, 3])
+@pytest.mark.parametrize("D", [32, 72, 96, 128])
+@pytest.mark.parametrize("L,lens", [(100, [100, 0, 17, 100]), (250, [250, 130, 0, 0]), (700, [0, 700, 1, 333])])
+def test_cross_many_items_per_block(budget, D, L, lens):
+    """One block and three walk all items: keys that stay and keys that stream, sets without keys between others,
+    items of one, two and three row tiles, frames of one stride and frames with a gap."""
+    H, Hkv = 2, 1
+    k, v = rand(130, 4, L, Hkv, D), rand(131, 4, L, Hkv, D)
+    n = torch.tensor(lens, dtype=torch.int32)
+    sets = sets_of(k, v, n)
+    for i, m in enumerate(lens):
+        k[i, m:], v[i, m:] = float("nan"), float("inf")
+    for T, S, gap in ((1, 460, 0), (3, 140, 9)):
+        q = rand(132, 4, T, S + gap, H, D)[:, :, :S]
+        o = torch.zeros(4, T, S + gap, H, D, dtype=BF, device="cuda")
+        lse = torch.full((4, T, H, S), float("nan"), device="cuda")
+        st.st_set_sm_budget(budget)
+        try:
+            st.st_attn_cross(q, k, v, o[:, :, :S], lse, kv_len=n.cuda())
+            assert st.st_check_device_status() == st.ST_OK
+        finally:
+            st.st_set_sm_budget(0)
+        check_attn(q, [sets], o[:, :, :S], lse, what=f"T{T}")
+        assert not o[:, :, S:].any()
+        o2, lse2 = torch.zeros_like(o), torch.zeros_like(lse)
+        st.st_attn_cross(q, k, v, o2[:, :, :S], lse2, kv_len=n.cuda())
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n_sets", [40, 70, 200])
+@pytest.mark.parametrize("D,S", [(72, 1), (128, 1), (72, 150), (128, 150)])
+def test_cross_many_sets(dtype, n_sets, D, S):
+    """More sets than a block keeps ranges of, as lengths and packed."""
+    L, H = 90, 1
+    n = torch.randint(0, L + 1, (n_sets,), generator=torch.Generator().manual_seed(133)).int()
+    n[:3] = torch.tensor([L, 0, 1])
+    q = rand(134, n_sets, 1, S, H, D, dtype=dtype)
+    k, v = rand(135, n_sets, L, H, D, dtype=dtype), rand(136, n_sets, L, H, D, dtype=dtype)
+    o, lse, _ = run_cross(q, k, v, kv_len=n.cuda())
+    check_attn(q, [sets_of(k, v, n)], o, lse, what="lengths")
+    off = torch.zeros(n_sets + 1, dtype=torch.int32)
+    off[1:] = n.cumsum(0)
+    kp, vp = k.flatten(0, 1), v.flatten(0, 1)
+    o, lse, _ = run_cross(q, kp, vp, kv_offsets=off.cuda(), max_len=L)
+    check_attn(q, [sets_of(kp, vp, offsets=off)], o, lse, what="packed")
+
+
+@pytest.mark.parametrize("budget", [1, 2])
+@pytest.mark.parametrize("H,Hkv,D,S,L", [(3, 3, 72, 5, 2600), (4, 2, 128, 1, 2300), (2, 1, 64, 70, 1700), (2, 2, 96, 130, 1300)])
+def test_cross_split_parts_on_few_blocks(budget, H, Hkv, D, S, L):
+    """The parts of split keys one behind another on one block, some of them empty: the bits of the whole GPU's run."""
+    lens = torch.tensor([L, 0, 300], dtype=torch.int32)
+    q, k, v = rand(140, 3, 1, S, H, D), rand(141, 3, L, Hkv, D), rand(142, 3, L, Hkv, D)
+    o, lse, n = run_cross(q, k, v, kv_len=lens.cuda())
+    assert n > 0
+    check_attn(q, [sets_of(k, v, lens)], o, lse, what="split")
+    st.st_set_sm_budget(budget)
+    try:
+        o2, lse2, n2 = run_cross(q, k, v, kv_len=lens.cuda())
+    finally:
+        st.st_set_sm_budget(0)
+    assert n2 == n and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("B,L", [(3, 300), (16, 200), (17, 200)])
+def test_cross_cut_by_cost(B, L):
+    """Many items of sets of very different lengths; one set more than the cut by cost takes."""
+    H, D, S = 2, 72, 2000
+    n = torch.randint(0, L + 1, (B,), generator=torch.Generator().manual_seed(143)).int()
+    n[0], n[1] = L, 0
+    q, k, v = rand(144, B, 1, S, H, D), rand(145, B, L, H, D), rand(146, B, L, H, D)
+    st.st_set_sm_budget(7)
+    try:
+        o, lse, _ = run_cross(q, k, v, kv_len=n.cuda())
+    finally:
+        st.st_set_sm_budget(0)
+    check_attn(q, [sets_of(k, v, n)], o, lse, what="cut")
+
+
+@pytest.mark.parametrize("S", [1, 90])
+def test_cross_fp32_rows_off_16_bytes(S):
+    """fp32 rows need 4-byte alignment only: queries, keys and values one element on, odd strides."""
+    H, D, L = 2, 32, 600
+    def off(seed, n):
+        x = torch.empty(n * (H * D + 3) + 1, device="cuda")
+        t = x[1:].as_strided((1, n, H, D), (n * (H * D + 3), H * D + 3, D, 1))
+        t.copy_(rand(seed, 1, n, H, D, dtype=F32))
+        return t
+    q, k, v = off(150, S)[:, None], off(151, L), off(152, L)
+    o = off(153, S)[:, None]
+    n = st.st_attn_cross_workspace_bytes(q, k)
+    st.st_attn_cross(q, k, v, o, workspace=workspace(n))
+    check_attn(q, [sets_of(k, v)], o, None, what="off")
+    st.st_attn_prefix(q, k[:, :70], v[:, :70], k[:, 70:], v[:, 70:], o)
+    check_attn(q, [sets_of(k, v)], o, None, what="prefix off")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_cross_offsets_beyond_32_bits(dtype):
+    """A cache whose rows lie 2^31 elements and more behind the first."""
+    L, step, H, D = 600, 2 ** 22, 2, 72
+    def cache(seed):
+        big = torch.empty(L * step, dtype=dtype, device="cuda")
+        t = big.as_strided((1, L, H, D), (L * step, step, D, 1))
+        t.copy_(rand(seed, 1, L, H, D, dtype=dtype))
+        return t
+    k, v = cache(160), cache(161)
+    q = rand(162, 1, 1, 3, H, D, dtype=dtype)
+    o, lse, _ = run_cross(q, k, v)
+    check_attn(q, [sets_of(k.contiguous(), v.contiguous())], o, lse, what="long cache")
+    # own keys of samples that share a prefix, left to the combine kernel
+    kp, vp = rand(163, 1, 50, H, D, dtype=dtype), rand(164, 1, 50, H, D, dtype=dtype)
+    ko, vo = (x.view(1, L, H, D).as_strided((2, L // 2, H, D), (L // 2 * step, step, D, 1)) for x in (k, v))
+    q = rand(165, 2, 1, 1, H, D, dtype=dtype)
+    o, lse, _ = run_prefix(q, kp, vp, ko, vo)
+    check_attn(q, [sets_of(kp, vp), sets_of(ko.contiguous(), vo.contiguous())], o, lse, what="own keys")
+
+
+@pytest.mark.parametrize("D", [72, 128])
+@pytest.mark.parametrize("B,S,H,Hkv,Lp,L", [(40, 1, 4, 2, 2000, 130), (5, 30, 2, 2, 1000, 30), (130, 1, 2, 2, 90, 17)])
+def test_prefix_packed_samples(D, B, S, H, Hkv, Lp, L):
+    """Samples packed over a long prefix (one tile and several), own keys of every length beside it."""
+    n = torch.randint(0, L + 1, (B,), generator=torch.Generator().manual_seed(170)).int()
+    n[0], n[1] = L, 0
+    q = rand(171, B, 1, S, H, D)
+    kp, vp = rand(172, 1, Lp, Hkv, D), rand(173, 1, Lp, Hkv, D)
+    k, v = rand(174, B, L, Hkv, D), rand(175, B, L, Hkv, D)
+    segs = [sets_of(kp, vp), sets_of(k, v, n)]
+    for i, m in enumerate(n.tolist()):
+        k[i, m:], v[i, m:] = float("nan"), float("nan")
+    o, lse, ws = run_prefix(q, kp, vp, k, v, kv_len=n.cuda())
+    assert ws > 0
+    check_attn(q, segs, o, lse, what="packed")
+    st.st_set_sm_budget(2)
+    try:
+        o2, lse2, _ = run_prefix(q, kp, vp, k, v, kv_len=n.cuda())
+    finally:
+        st.st_set_sm_budget(0)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
