@@ -42,6 +42,24 @@ __device__ __forceinline__ KvRange kv_range(const KvSeg &g, int b) {
   return r;
 }
 
+// Keys up to the last of the first n that the mask lets count (a warp's answer,
+// looked for from the end, 256 at a time).
+__device__ __forceinline__ int last_key(const unsigned char *mask, int n, int lane) {
+#pragma unroll 1
+  while (n > 0) {
+    int last = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = n - 1 - lane - 32 * i;
+      if (k >= 0 && mask[k]) last = max(last, k + 1);
+    }
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (last) return last;
+    n -= 256;
+  }
+  return 0;
+}
+
 struct CondParams {
   Geom g;                      // Q and O by unit: g.B batches (or groups of batches) of g.T frames of R0 rows
   int R0;                      // query rows of a unit (g.S)

@@ -66,6 +66,8 @@ __global__ void __launch_bounds__(NT) cond_simt_kernel(const __grid_constant__ s
     sg.len = st::after_wait(sg.len);
     sg.offsets = st::after_wait(sg.offsets);
     kr[g] = st::kv_range(sg, st::cond_batch(p, unit));
+    // (every warp looks for itself: the padding behind a prompt costs nothing)
+    if (sg.mask) kr[g].n = st::last_key(st::after_wait(sg.mask) + (long long)kr[g].set * sg.L, kr[g].n, tid & 31);
     steps[g] = (kr[g].n + BN - 1) / BN;
   }
   const long long total = (long long)steps[0] + steps[1];

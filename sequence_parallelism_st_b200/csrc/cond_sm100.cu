@@ -690,15 +690,27 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   // scheduled, then wait for the previous one before any global access
   pdl_trigger();
   pdl_wait();
-#pragma unroll
-  for (int g = 0; g < 2; ++g)
-    if (g < a.c.n_seg && a.c.seg[g].n_sets <= K::TABLE && int(threadIdx.x) < a.c.seg[g].n_sets) {
-      st::KvSeg sg = a.c.seg[g];
-      sg.len = st::after_wait(sg.len);
-      sg.offsets = st::after_wait(sg.offsets);
-      const st::KvRange r = st::kv_range(sg, int(threadIdx.x) * sg.per);
-      sSet[g * K::TABLE + threadIdx.x] = make_int2(r.row0, r.n);
+  // the sets' key ranges; a warp per set looks where a mask's last key is, so that
+  // the padding behind a prompt costs nothing
+#pragma unroll 1
+  for (int g = 0; g < a.c.n_seg; ++g) {
+    st::KvSeg sg = a.c.seg[g];
+    if (sg.n_sets > K::TABLE) continue;
+    sg.len = st::after_wait(sg.len);
+    sg.offsets = st::after_wait(sg.offsets);
+    if (!sg.mask) {
+      if (int(threadIdx.x) < sg.n_sets) {
+        const st::KvRange r = st::kv_range(sg, int(threadIdx.x) * sg.per);
+        sSet[g * K::TABLE + threadIdx.x] = make_int2(r.row0, r.n);
+      }
+      continue;
     }
+#pragma unroll 1
+    for (int set = warp; set < sg.n_sets; set += K::THREADS / 32) {
+      const int n = st::last_key(st::after_wait(sg.mask) + (long long)set * sg.L, st::kv_range(sg, set * sg.per).n, lane);
+      if (lane == 0) sSet[g * K::TABLE + set] = make_int2(0, n);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -984,16 +996,19 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           const uint32_t ph = ring.phase(resident, j);
           const Step sp = step_of<BN>(it, j);
           const unsigned char *mk = a.c.seg[sp.seg].mask;
-          const bool work = j < it.n_kv && (K::ONES || sp.valid < BN || mk);
+          const bool real = j < it.n_kv;
           bool keep[(BN + 31) / 32];
-          if (work) {                          // before the wait: the mask bytes are on their way
+          bool dead = false;                   // the tile has rows to clear
+          if (real) {                          // before the wait: the mask bytes are on their way
             if (mk) mk += (long long)sp.set * a.c.seg[sp.seg].L + sp.key;
 #pragma unroll
             for (int i = 0; i < (BN + 31) / 32; ++i) {
               const int r = lane + 32 * i;
               keep[i] = r < sp.valid && (!mk || st::after_wait(mk)[r]);
+              dead |= !keep[i] && (BN % 32 == 0 || r < BN);
             }
           }
+          const bool work = real && (K::ONES || __any_sync(0xffffffffu, dead));
           if (lane == 0) ok = mbar_wait(v_full + bar, ph, epoch);
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
           if (!ok) break;

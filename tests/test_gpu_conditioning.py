@@ -627,3 +627,21 @@ def test_prefix_packed_samples(D, B, S, H, Hkv, Lp, L):
     finally:
         st.st_set_sm_budget(0)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,S", [(72, 400), (128, 400), (72, 1)])
+def test_cross_masks_with_dead_tails(dtype, D, S):
+    """Masks whose last key is anywhere from none to the end of 1,300, at the end of the looks of 256 among them."""
+    last = [0, 1, 255, 256, 257, 276, 277, 1043, 1044, 1045, 1299, 1300]
+    B, L, H = len(last), 1300, 1
+    q, k, v = rand(180, B, 1, S, H, D, dtype=dtype), rand(181, B, L, H, D, dtype=dtype), rand(182, B, L, H, D, dtype=dtype)
+    keep = torch.zeros(B, L, dtype=torch.bool)
+    for i, n in enumerate(last):
+        keep[i, max(0, n - 700):n:3] = True
+        if n:
+            keep[i, n - 1] = True
+    sets = sets_of(k, v, mask=keep)
+    k[~keep], v[~keep] = float("nan"), float("inf")
+    o, lse, _ = run_cross(q, k, v, kv_mask=keep.cuda())
+    check_attn(q, [sets], o, lse, what="tails")
