@@ -10,7 +10,9 @@
 //     a K/V tile is read once for its whole group.
 //   * Few work items: the keys are split into parts whose fp32 partials go to
 //     the workspace and are combined by a second kernel, as attn_chunk_merge
-//     does (same formula), so that one query over long states still uses every SM.
+//     does (same formula), so that one query over long states still uses every SM
+//     (2 x 24 heads of 128 channels on 8 KV heads, 20,736 keys: 41 us of 26 us
+//     that reading the states takes).
 //   * Samples of at most PACK_ROWS rows that share a prefix attend to it in
 //     packed tiles; the combine kernel attends each row's own keys.
 #include <math.h>
@@ -23,11 +25,19 @@ using st::CondParams;
 using st::Geom;
 using st::KvSeg;
 
-// Rows per sample (heads of a group included) up to which the samples of a
-// prefix are packed.
+// Samples of a prefix are packed up to this many rows each (heads of a group
+// included), and only where the prefix is longer than rows x own keys: the
+// combine kernel reads a sample's own keys once per row.  64 samples, 16 heads
+// x 72, 64 own keys, packed and not: prefix of 4096, 1 row 31 and 461 us, 8 rows
+// 86 and 461, 32 rows 275 and 461; prefix of 512, 32 rows 194 and 87.
 constexpr int PACK_ROWS = 32;
-constexpr int MAX_SPLIT = 64;
-constexpr int MIN_KEYS = 256;  // keys of a part at least
+// Parts of split keys: at most MAX_SPLIT (two per lane of the combine kernel),
+// of MIN_KEYS keys at least, from SPLIT_KEYS keys on, or fewer where there is
+// little to combine.  16 heads x 72, split and not: 1 row of 4 batches, 600
+// keys 15.5 and 15.8 us, 1200 keys 19.6 and 23.8; 64 rows of 2 batches, 600 keys
+// 20.4 and 15.6; 200 rows, 1200 keys 23 and 30.
+constexpr int MAX_SPLIT = 64, MIN_KEYS = 256, SPLIT_KEYS = 1024;
+constexpr int FEW_ROWS = 1024, SPLIT_KEYS_FEW = 640;
 
 bool d_supported(int D) { return D == 32 || D == 64 || D == 72 || D == 80 || D == 96 || D == 128; }
 
@@ -122,7 +132,8 @@ st_status make_plan(const st_attn_desc *desc, const st_kv_desc *d0, const st_kv_
   // batches that share every key they attend, or (few rows) their prefix
   const bool follow = flat && g.sb == (long long)g.S * g.ss;
   const bool share = !d1 && seg0.per > 1 && follow;
-  const bool pack = with_ws && d1 && seg0.per > 1 && follow && (long long)g.S * grp <= PACK_ROWS;
+  const bool pack = with_ws && d1 && seg0.per > 1 && follow && (long long)g.S * grp <= PACK_ROWS &&
+                    seg0.L > (long long)g.S * grp * seg1.L;
   if (share || pack) {
     p.bm = seg0.per;
     if (pack) {
@@ -146,17 +157,20 @@ st_status make_plan(const st_attn_desc *desc, const st_kv_desc *d0, const st_kv_
   p.scale = desc->scale > 0.f ? desc->scale : 1.0f / sqrtf((float)g.D);
   p.o_f32 = desc->o_fp32 || !bf16;
   pl.dtype = desc->dtype;
-  // split the keys when the items leave more than half of the GPU idle; items
+  // split long keys when the items leave more than half of the GPU idle; items
   // of one row tile then take one part of their keys with each of their tiles
   const st::CondTile t = bf16 ? st::cond_tile(g.D) : st::CondTile{64, 1, 64};
-  long long steps = 0;
-  for (int i = 0; i < p.n_seg; ++i) steps += ceil_div(p.seg[i].L, t.keys);
+  long long steps = 0, keys = 0;
+  for (int i = 0; i < p.n_seg; ++i) {
+    steps += ceil_div(p.seg[i].L, t.keys);
+    keys += p.seg[i].L;
+  }
   const int tile_rows = bf16 ? t.rows / p.G * p.G : t.rows;
   const long long items = (long long)st::cond_units(p) * p.HW * ceil_div(p.R, tile_rows * t.tiles);
   const long long cap = (long long)st::device_sms() * (bf16 ? 1 : 2);
   p.n_split = p.spread = 1;
   const long long min_steps = ceil_div(MIN_KEYS, t.keys);
-  if (with_ws && items * 2 <= cap && steps >= 2 * min_steps) {
+  if (with_ws && items * 2 <= cap && keys >= (p.part_rows <= FEW_ROWS ? SPLIT_KEYS_FEW : SPLIT_KEYS)) {
     if (p.R <= tile_rows) p.spread = t.tiles;
     long long n = cap / items;
     if (n > steps / min_steps) n = steps / min_steps;

@@ -5,36 +5,52 @@
 //   masks read on the device.
 //
 // What bounds it.  The keys of a text prompt are few, so an item is short: at
-// head dim 72 a 128 x 64 step is about 420 cycles of tensor work (S with
-// both operands in shared memory, PV with P in TMEM) against 512 cycles of
-// special-function unit for its exponentials, and below about 190 keys reading
-// Q and writing O takes longer than either.  The chain S -> softmax -> PV -> S
-// of one tile leaves every unit idle most of the time, so several row tiles run
-// side by side, each with its own chain.
+// head dim 72 a 128 x 80 step is about 400 cycles of tensor work (S with
+// both operands in shared memory, PV with P in TMEM) against 640 cycles of
+// special-function unit for its exponentials, of which a quarter go to the FMA
+// pipe, and below about 190 keys reading Q and writing O takes longer than
+// either.  The chain S -> softmax -> PV -> S of one tile leaves every unit idle
+// most of the time, so several row tiles run side by side, each with its own
+// chain; what is left is the latency of the hand-overs between them (tensor
+// pipe 32%, special-function unit 39% busy at 320 keys).  Second comes the
+// instruction cache: all roles together are 60 to 85 KB of code, and every
+// variant that shortened them got faster (16 heads x 72, 65,536 rows, 320 keys:
+// 176 us at 84 KB, 161 us at 71 KB).
 //
 // Design (one persistent CTA per SM, warp-specialised):
 //   * A work item is up to NT tiles of 128 rows of one (unit, head): three for
-//     head dims up to 96, whose S (64 keys) and O fit three times into the 512
-//     TMEM columns, two (128 keys per step) for 128.  A spatial kernel of two
-//     tiles with S double-buffered has the same number of scores in flight
-//     but two softmax warps per sub-partition; three warps hide more of each
-//     other's TMEM loads and barrier waits.
-//   * Each tile has one issuer thread.  S(j + 1) follows PV(j) in program order
+//     head dims up to 96, whose S (64 to 96 keys) and O fit three times into
+//     the 512 TMEM columns, two (128 keys per step) for 128.
+//   * Each tile has one issuer warp; S(j + 1) follows PV(j) in program order
 //     into the same TMEM columns (MMAs of one thread execute in order), so the
-//     chain has two hand-overs a step: S ready, P ready.
-//   * When every key tile of a launch fits the K/V ring, a CTA walks
+//     chain has two hand-overs a step: S ready, P ready.  One issuer for all
+//     tiles was bound by its own instructions (60 cycles an MMA).
+//   * The softmax warps (one thread per row) also divide O by the row sum and
+//     write it out: through the item's own Q tile, dead by then, with bulk tensor
+//     stores, or row by row (fp32 results, partials, heads packed into rows).
+//     Warps of their own for this were slower by 5% (more code, a hand-over).
+//   * The running maximum is raised (and O rescaled in TMEM) only when it grows
+//     by more than 2^8.
+//   * When every key tile of a launch fits the K/V stages, a CTA walks
 //     consecutive items and keeps K and V in shared memory until the set or the
-//     head changes; otherwise they stream through the ring.
-//   * One warp per V stage clears the rows of keys that do not count (which may
-//     hold NaN: 0 * NaN would reach O) and, where the head dim is padded, sets
-//     column D to 1 so that PV adds up the rounded weights.
-//   * Softmax: one thread per row, running max raised (and O rescaled in TMEM)
-//     only when it grows by more than 2^8; exponentials on the special-function
-//     unit with every fourth pair on the FMA pipe.
-//   * The epilogue warps divide O by the row sum and write it with bulk tensor
-//     stores, or row by row (fp32 partials, heads packed into rows).
+//     head changes; otherwise they stream through the stages (65,536 rows, 16
+//     heads x 72, 300 keys: 165 us kept, 200 us streamed through three stages).
+//   * Split keys and one row tile (a token per sample): the tiles of a CTA take
+//     the same rows and every NT-th step, one part each, so that NT chains run
+//     (64 samples of one token, 16 heads x 72, 16,384 shared keys: 93 us with one
+//     chain, 62 us with three; the combine kernel's share is in both).
+//   * V helpers clear the rows of keys that do not count (which may hold NaN:
+//     0 * NaN would reach O) and, where the head dim is padded, set column D to 1
+//     so that PV adds up the rounded weights.
 //   * Every wait is bounded; a wait that runs out sets an error word and an
 //     abort epoch, in-flight copies are drained, TMEM is freed.
+//
+// Measured (device time, 65,536 rows, 16 heads; the spatial kernel of this
+// library beside it needs 210 us for 256 keys of 72 channels):
+//   72 channels:  64 keys 89 us, 128 108 us, 320 156 us (618 TF/s), 1024 466 us
+//                 (663 TF/s), 4096 1607 us (770 TF/s)
+//   128 channels: 64 keys 147 us, 128 138 us, 320 316 us (540 TF/s), 1024 582 us
+//                 (944 TF/s), 4096 2040 us (1078 TF/s)
 #include <cuda.h>
 #include <math.h>
 #include <string.h>
@@ -408,7 +424,6 @@ struct alignas(16) Item {
   int fresh;                   // its keys are not those of the item before
   int release;                 // nor those of the item after
   int qb, qb_end;              // row block of the unit; end of its band
-  int pad[3];
 };
 constexpr int ITEMS = 4;       // items in flight between the scheduler and the others
 static_assert(ITEMS * sizeof(Item) <= 384, "item ring");
