@@ -287,7 +287,8 @@ typedef enum { ST_ROPE_INTERLEAVED = 0, ST_ROPE_HALVES = 1 } st_rope_pairing;
  * h_q or h_k may be 0 (that tensor is absent). */
 typedef struct {
   int size;               /* sizeof(st_qk_desc)                                 */
-  int n_tokens, h_q, h_k, D;   /* D a multiple of 8, at most 256                */
+  int n_tokens, h_q, h_k, D;   /* D a multiple of 8, at most 256; (h_q + h_k) D
+                             at most 2^30                                       */
   st_dtype dtype;         /* of Q, K and both outputs                           */
   float eps;              /* >= 0                                               */
   int pairing;            /* st_rope_pairing                                    */
@@ -330,7 +331,7 @@ st_status st_qk_norm_rope(const st_qk_desc *desc, const void *q, const void *k, 
  *     clamped to [0, n_rows].  Excludes len and mask.
  *   mask: optional u8 device [n_sets, L] dense, nonzero = the key counts.
  * Keys that do not count may hold anything, NaN and infinities included.
- * Rows of a mask's tail cost time; give len too where the tail is long. */
+ * Keys behind a mask's last one are not walked; holes cost what keys do. */
 typedef struct {
   int size;               /* sizeof(st_kv_desc)                                 */
   int n_sets, L;          /* n_sets divides B; L >= 1 (0 only with len NULL,

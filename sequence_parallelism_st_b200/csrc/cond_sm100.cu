@@ -102,8 +102,11 @@ template <int D> struct Cfg {
   // lanes then meet at most 2 to a bank), the other widths in the layout of Q.
   // At head dim 128 one of the four gives way to a fourth K/V tile where the
   // keys take more than one step (TIGHT): row tile 1 then runs a step behind
-  // row tile 0, in whose place its next Q goes.  (2 K and 1 V: 955 TF/s over
-  // 4096 keys.  K and V in turn in three tiles: 874.)
+  // row tile 0, in whose place its next Q goes, and stays there, which keeps the
+  // two chains out of step.  (TF/s over 4096 and 300 keys: 1078 and 522 so; 2 K and
+  // 1 V 955 and 532; K and V in turn in three tiles 874 and 556; O staged apart
+  // from one Q tile each, the chains in step, 886 and 528, with row tile 1 held
+  // back by 2 steps 924 and 505.)
   static constexpr int NQ = 2 * NT;
   static constexpr bool TIGHT = D == 128;
   static constexpr bool DENSE = D == 72 || D == 80;

@@ -305,6 +305,7 @@ ST_API st_status st_qk_norm_rope(const st_qk_desc *d, const void *q, const void 
   if (d->n_tokens <= 0 || d->h_q < 0 || d->h_k < 0 || d->h_q + (long long)d->h_k <= 0 || d->D <= 0 || d->pos_period < 0)
     return ST_ERR_SHAPE;
   if (!(d->eps >= 0.f)) return ST_ERR_SHAPE;
+  if (((long long)d->h_q + d->h_k) * d->D > (1LL << 30)) return ST_ERR_SHAPE;
   if (d->dtype != ST_F32 && d->dtype != ST_BF16) return ST_ERR_DTYPE;
   if (d->pairing != ST_ROPE_INTERLEAVED && d->pairing != ST_ROPE_HALVES) return ST_ERR_SHAPE;
   if (d->D % 8 || d->D > 256) return ST_ERR_UNSUPPORTED;

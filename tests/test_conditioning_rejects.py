@@ -130,3 +130,8 @@ def test_binding_checks():
     assert code(st.st_qk_norm_rope, x, q_gamma=torch.ones(15)) == st.ST_ERR_SHAPE
     assert code(st.st_qk_norm_rope, x, rope_table=torch.zeros(6, 16)) == st.ST_ERR_NULL
     assert code(st.st_qk_norm_rope, x, positions=torch.zeros(6, dtype=torch.int64)) == st.ST_ERR_DTYPE
+
+
+def test_qk_norm_rope_rejects_rows_beyond_its_indices():
+    assert qk(h_q=(1 << 30) // 72 + 1, k=None, ko=None, h_k=0, n_tokens=1) == st.ST_ERR_SHAPE
+    assert qk(h_q=2 ** 31 - 1, h_k=2 ** 31 - 1, n_tokens=1, D=8) == st.ST_ERR_SHAPE
