@@ -355,10 +355,16 @@ def _device_call(where, fn, device, stream, *args):
     import torch
     if device.type != "cuda":
         raise StattnError(ST_ERR_NULL, f"{where}: tensors must be on a CUDA device")
+    # (the raw handle: a Stream object costs 3 us a call)
+    s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
     if device.index == torch.cuda.current_device():
-        return fn(*args, _stream(stream))
+        return fn(*args, s)
     with torch.cuda.device(device):
-        return fn(*args, _stream(stream))
+        return fn(*args, s)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 # The checks below run on every call and build their messages only when they fail.
@@ -447,9 +453,9 @@ def st_qk_norm_rope(q, k=None, q_out=None, k_out=None, q_gamma=None, k_gamma=Non
         if rope_table.dtype != torch.float32 or not rope_table.is_contiguous() or rope_table.numel() != n_pos * head_dim:
             raise StattnError(ST_ERR_SHAPE, f"{where}: rope_table is fp32 [n, D / 2, 2]")
     pos = _int32(where, positions, tokens, index)
-    r = _device_call(where, _c["st_qk_norm_rope"], x.device, stream, ctypes.byref(d), _ptr(q), _ptr(k),
-                     _ptr(q if q_out is None else q_out), _ptr(k if k_out is None else k_out), _ptr(q_gamma),
-                     _ptr(k_gamma), _ptr(rope_table), n_pos, pos)
+    r = _device_call(where, _c["st_qk_norm_rope"], x.device, stream, ctypes.byref(d), _addr(q), _addr(k),
+                     _addr(q if q_out is None else q_out), _addr(k if k_out is None else k_out), _addr(q_gamma),
+                     _addr(k_gamma), _addr(rope_table), n_pos, pos)
     return r if raw else _check(r, where)
 
 
@@ -524,7 +530,7 @@ def _workspace(where, t, device):
         return None, 0
     if t.device != device or not t.is_contiguous():
         raise StattnError(ST_ERR_SHAPE, f"{where}: workspace")
-    return _ptr(t), t.numel() * t.element_size()
+    return _addr(t), t.numel() * t.element_size()
 
 
 def _check_out(where, q, o, lse, o_fp32):
@@ -552,7 +558,7 @@ def st_attn_cross(q, k, v, o, lse=None, *, kv_len=None, kv_offsets=None, kv_mask
     kv = _kv_desc("st_attn_cross", desc.D, q, k, v, kv_len, kv_offsets, kv_mask, max_len)
     ws, n = _workspace("st_attn_cross", workspace, q.device)
     r = _device_call("st_attn_cross", _c["st_attn_cross"], q.device, stream, ctypes.byref(desc), ctypes.byref(kv),
-                     _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), ws, n)
+                     _addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), ws, n)
     return r if raw else _check(r, "st_attn_cross")
 
 
@@ -578,7 +584,7 @@ def st_attn_prefix(q, k_prefix, v_prefix, k, v, o, lse=None, *, prefix_len=None,
     kv = _kv_desc("st_attn_prefix", desc.D, q, k, v, kv_len, kv_offsets, kv_mask, max_len)
     ws, n = _workspace("st_attn_prefix", workspace, q.device)
     r = _device_call("st_attn_prefix", _c["st_attn_prefix"], q.device, stream, ctypes.byref(desc), ctypes.byref(pre),
-                     ctypes.byref(kv), _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
+                     ctypes.byref(kv), _addr(q), _addr(k_prefix), _addr(v_prefix), _addr(k), _addr(v), _addr(o), _addr(lse),
                      ws, n)
     return r if raw else _check(r, "st_attn_prefix")
 
