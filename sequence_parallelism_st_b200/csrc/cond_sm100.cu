@@ -75,7 +75,7 @@ constexpr unsigned long long WAIT_NS = 2000000000ull;  // a drain's limit: 2 s
 constexpr uint32_t WAIT_CLOCKS = 3800000000u;          // a wait's: 2 s at 1.9 GHz
 constexpr float NO_KEY = -3.0e38f;           // running max of a row no key counted for yet
 
-template <int D> struct Cfg {
+template <int D, bool MIX = false> struct Cfg {
   static constexpr int NT = D <= 96 ? 3 : 2;           // row tiles in flight
   static constexpr int BN = D <= 64 ? 96 : (D <= 80 ? 80 : (D <= 96 ? 64 : 128));   // keys per step
   static constexpr int CH = BN / 16;                   // chunks of 16 keys (a K slice of PV)
@@ -88,11 +88,19 @@ template <int D> struct Cfg {
   static constexpr int QTILE = QT0 + BLOCK_M * SW1;
   static constexpr int KT0 = BN * SW0;
   static constexpr int KBYTES = KT0 + BN * SW1, KTILE = (KBYTES + 1023) / 1024 * 1024;   // a 128B swizzle starts at 1 KB
-  // V as column atoms of VW elements (MN-major), PV one MMA of N = DPV per 16 keys
-  static constexpr int VW = (D == 72 || D == 80) ? 16 : ((D == 96 || D == 32) ? 32 : 64);
-  static constexpr int DPV = ((D + VW - 1) / VW) * VW;
-  static constexpr int VA = DPV / VW, VSW = VW * 2, VAT = BN * VSW, VTILE = VA * VAT;
-  static_assert(QTILE % 1024 == 0 && VTILE % (8 * VSW) == 0, "swizzle atoms");
+  // V as VA column atoms of VW elements (MN-major), PV one MMA of N = DPV per 16
+  // keys.  MIX (spread items of 72 to 96 channels, whose V is read by one tile
+  // only and so bound by the rows of its boxes): an atom of 64 and one of VR, two
+  // MMAs.  (16,384 keys, 64 rows, 16 heads x 72: 35 us so, 42 us in atoms of 16;
+  // 65,536 rows, 4096 keys: 1669 us so, 1607 us in atoms of 16.)
+  static constexpr int VW = MIX ? 64 : (D == 72 || D == 80) ? 16 : ((D == 96 || D == 32) ? 32 : 64);
+  static constexpr int VA = MIX ? 1 : (D + VW - 1) / VW, NV0 = VA * VW;
+  static constexpr int VR = MIX ? (D - 64 + 15) / 16 * 16 : 0, VRX = VR ? VR : 16, DPV = NV0 + VR;
+  static constexpr int VSW = VW * 2, VAT = BN * VSW, VSWR = VRX * 2, VT0 = VA * VAT;
+  static constexpr int VBYTES = VT0 + BN * VR * 2, VTILE = MIX ? (VBYTES + 1023) / 1024 * 1024 : VBYTES;
+  static_assert(QTILE % 1024 == 0 && VT0 % (8 * VSW) == 0, "swizzle atoms");
+  // where column D of a row lies: the ones
+  static constexpr int ONE_AT = MIX ? VT0 : D / VW * VAT, ONE_SW = MIX ? VSWR : VSW, ONE_X = (D - (MIX ? 64 : D / VW * VW)) * 2;
   static constexpr bool ONES = DPV > D;
   static constexpr int TW = BN + DPV;                  // TMEM columns of a tile: S (P over it), O
   static_assert(NT * TW <= 512, "TMEM");
@@ -387,7 +395,7 @@ template <int BYTES> __device__ __forceinline__ int swz(int r, int f) {
 // ---------------------------------------------------------------- work items
 struct Maps {
   CUtensorMap q0, q1;          // the head's first C0 channels, the rest
-  CUtensorMap k0[2], k1[2], v[2];
+  CUtensorMap k0[2], k1[2], v[2], vr[2];      // K alike; V's atoms, the rest of V
   CUtensorMap o0, o1;
 };
 
@@ -640,10 +648,10 @@ __device__ __forceinline__ int own_slot(bool spread, int X, uint32_t n) { return
 // TIGHT: slot `i` of the Q tiles after slot q0.
 __device__ __forceinline__ int q_slot(int q0, int i, int nq) { return q0 + i >= nq ? q0 + i - nq : q0 + i; }
 
-template <int D>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+template <int D, bool MIX>
+__global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
     cond_attn_sm100(const __grid_constant__ Maps mp, const __grid_constant__ Args a) {
-  using K = Cfg<D>;
+  using K = Cfg<D, MIX>;
   constexpr int NT = K::NT, NB = K::NB, NQ = K::NQ, BN = K::BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -842,11 +850,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             if (load_kv) {
               if (wait && !(ok = mbar_wait(v_empty + was, ph, epoch))) break;
               if (real) {
-                mbar_expect_tx(v_full + bar, K::VTILE);
+                mbar_expect_tx(v_full + bar, K::VBYTES);
                 uint8_t *dv = sV + st * K::VTILE;
 #pragma unroll 1
                 for (int t = 0; t < K::VA; ++t)
                   tma_load_4d(dv + t * K::VAT, &mp.v[g], v_full + bar, t * K::VW, it.kvh, sp.row + sp.key, set);
+                if (MIX) tma_load_4d(dv + K::VT0, &mp.vr[g], v_full + bar, K::NV0, it.kvh, sp.row + sp.key, set);
               } else {
                 mbar_arrive(v_full + bar);
               }
@@ -954,12 +963,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             const uint32_t va = sdesc_lo<K::VAT>(aV + st * K::VTILE);
             if (!(ok = mbar_wait(p_full + X, steps & 1, epoch))) break;
             tc_fence_after();
-            constexpr uint32_t IDPV = idesc_bf16(BLOCK_M, K::DPV, 0, 1);
+            constexpr uint32_t IDPV = idesc_bf16(BLOCK_M, K::NV0, 0, 1), IDVR = idesc_bf16(BLOCK_M, K::VRX, 0, 1);
+            const uint32_t vr = sdesc_lo<16>(aV + st * K::VTILE + K::VT0);
 #pragma unroll
             for (int kk = 0; kk < K::CH; ++kk)
-              if (kk < nk)
-                mma_ts(lead, dO, dS + kk * 8, sdesc<8 * K::VSW, layout_of(K::VSW)>(va + kk * K::VSW), IDPV,
-                       (j > j0 || kk > 0) ? 1u : 0u);
+              if (kk < nk) {
+                const uint32_t acc = (j > j0 || kk > 0) ? 1u : 0u;
+                mma_ts(lead, dO, dS + kk * 8, sdesc<8 * K::VSW, layout_of(K::VSW)>(va + kk * K::VSW), IDPV, acc);
+                if (MIX)
+                  mma_ts(lead, dO + K::NV0, dS + kk * 8, sdesc<8 * K::VSWR, layout_of(K::VSWR)>(vr + kk * K::VSWR), IDVR, acc);
+              }
             if (last) tc_commit(lead, o_full + X);
             if (cur.release) tc_commit(lead, v_empty + bar);
           }
@@ -991,7 +1004,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       __syncwarp();
     } else if (warp >= K::W_FIX && warp < K::W_FIX + K::NF) {
       // ================= V rows of keys that do not count; ones column =================
-      constexpr int A1 = K::ONES ? D / K::VW : 0, XB = (D % K::VW) * 2;
       bool ok = true;
       Ring<NB> ring;
       Reader rd;
@@ -1041,8 +1053,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 #pragma unroll
                   for (int f = 0; f < K::VSW / 16; ++f)
                     *reinterpret_cast<uint4 *>(vt + t * K::VAT + r * K::VSW + f * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int f = 0; f < K::VR / 8; ++f)
+                  *reinterpret_cast<uint4 *>(vt + K::VT0 + r * K::VSWR + f * 16) = make_uint4(0, 0, 0, 0);
               } else if (K::ONES) {
-                *reinterpret_cast<uint16_t *>(vt + A1 * K::VAT + r * K::VSW + (swz<K::VSW>(r, XB >> 4) << 4) + (XB & 15)) =
+                *reinterpret_cast<uint16_t *>(vt + K::ONE_AT + r * K::ONE_SW + (swz<K::ONE_SW>(r, K::ONE_X >> 4) << 4) + (K::ONE_X & 15)) =
                     0x3F80;                    // bf16 1.0
               }
             }
@@ -1379,8 +1394,8 @@ bool map_kv(CUtensorMap *m, const void *ptr, const st::CondParams &p, const st::
 
 std::atomic<uint32_t> g_epoch{0};
 
-template <int D> st_status launch(const st::CondParams &p, cudaStream_t s) {
-  using K = Cfg<D>;
+template <int D, bool MIX = false> st_status launch(const st::CondParams &p, cudaStream_t s) {
+  using K = Cfg<D, MIX>;
   Args a = {};
   a.c = p;
   a.tile_rows = BLOCK_M / p.G * p.G;
@@ -1407,7 +1422,8 @@ template <int D> st_status launch(const st::CondParams &p, cudaStream_t s) {
     if (!sg.L) continue;                       // no keys: never loaded
     if (!map_kv(&m.k0[g], sg.k, p, sg, K::C0, K::SW0, K::BN) ||
         (K::C1 && !map_kv(&m.k1[g], sg.k, p, sg, K::C1X, K::SW1X, K::BN)) ||
-        !map_kv(&m.v[g], sg.v, p, sg, K::VW, K::VSW, K::BN))
+        !map_kv(&m.v[g], sg.v, p, sg, K::VW, K::VSW, K::BN) ||
+        (MIX && !map_kv(&m.vr[g], sg.v, p, sg, K::VRX, K::VSWR, K::BN)))
       return ST_ERR_CUDA;
   }
   if (steps * (a.n_split + 1) >= (1LL << 31)) return ST_ERR_SHAPE;
@@ -1441,7 +1457,7 @@ template <int D> st_status launch(const st::CondParams &p, cudaStream_t s) {
     a.dband_last = st::make_fastdiv(uint32_t(a.band_last));
     a.dbandcols = st::make_fastdiv(uint32_t(a.band) * uint32_t(a.cols));
   }
-  auto kern = cond_attn_sm100<D>;
+  auto kern = cond_attn_sm100<D, MIX>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM) != cudaSuccess)
     return ST_ERR_CUDA;
   // A build that grants fewer registers than the split assumes would wait in
@@ -1489,9 +1505,9 @@ st_status cond_sm100(const CondParams &p, cudaStream_t s) {
   switch (p.g.D) {
     case 32: return launch<32>(p, s);
     case 64: return launch<64>(p, s);
-    case 72: return launch<72>(p, s);
-    case 80: return launch<80>(p, s);
-    case 96: return launch<96>(p, s);
+    case 72: return p.spread > 1 ? launch<72, true>(p, s) : launch<72>(p, s);
+    case 80: return p.spread > 1 ? launch<80, true>(p, s) : launch<80>(p, s);
+    case 96: return p.spread > 1 ? launch<96, true>(p, s) : launch<96>(p, s);
     case 128: return launch<128>(p, s);
   }
   return ST_ERR_UNSUPPORTED;
