@@ -205,7 +205,7 @@ __device__ __forceinline__ void axpy4(float4 &a, float w, const float4 &x) {
 constexpr int BATCH = 8;       // loads of a lane in flight
 
 template <typename T, bool OWN, int WPR>
-__global__ void __launch_bounds__(128, WPR == 4 ? 8 : 4) cond_combine(const __grid_constant__ CondParams p) {
+__global__ void __launch_bounds__(128, WPR == 4 && sizeof(T) == 2 ? 8 : 4) cond_combine(const __grid_constant__ CondParams p) {
   __shared__ __align__(16) float sq[4][128];
   __shared__ float sm[4], sl[4];
   constexpr float L2E = 1.4426950408889634f;
@@ -214,12 +214,17 @@ __global__ void __launch_bounds__(128, WPR == 4 ? 8 : 4) cond_combine(const __gr
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
   const int sub = wp % WPR;                    // this warp's share of the row
   const int D = p.g.D, d0 = 4 * lane, nd = D - d0;
-  const long long row = (long long)blockIdx.x * (4 / WPR) + wp / WPR;
+  const uint32_t row = blockIdx.x * (4 / WPR) + wp / WPR;    // (rows of a call: below 2^31)
   if (row >= p.part_rows) return;              // (WPR = 4: a block per row, none past the last)
-  const int r = int(row % p.R);
-  const int w = int(row / p.R % p.HW), unit = int(row / ((long long)p.R * p.HW));
+  const uint32_t col = row / uint32_t(p.R);
+  const int r = int(row - col * uint32_t(p.R)), unit = int(col / uint32_t(p.HW)), w = int(col) - unit * p.HW;
   const long long off = st::cond_row(p, unit, w, r);
   const float *part_lse = st::after_wait(p.part_lse), *part_o = st::after_wait(p.part_o);
+  // the parts of this warp: sub, sub + WPR, ... (at most 64 in all)
+  const int n = p.n_split;
+  const int c0 = sub + WPR * lane, c1 = c0 + 32 * WPR;
+  const float l0 = c0 < n ? part_lse[(long long)c0 * p.part_rows + row] : -INFINITY;
+  const float l1 = c1 < n ? part_lse[(long long)c1 * p.part_rows + row] : -INFINITY;
   float m = -INFINITY, l = 0.f;                // running max (log2 units) and sum; the same in all lanes
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if constexpr (OWN) {
@@ -244,6 +249,15 @@ __global__ void __launch_bounds__(128, WPR == 4 ? 8 : 4) cond_combine(const __gr
       const int key = k0 + (lane >> 1), half = lane & 1;     // two lanes per key, every other 8 channels each
       float x = 0.f;
       const bool on = key < kr.n && (!mk || mk[key]);
+      // V of the first keys is on its way with K (a key that does not count is not read)
+      const unsigned counts = __ballot_sync(0xffffffffu, on);
+      const T *vp = V + (long long)k0 * sg.stride_l + d0;
+      float4 x4[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        x4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (nd > 0 && (counts >> 2 * i & 1)) x4[i] = load4(vp + i * sg.stride_l, nd);
+      }
       if (on) {
         const T *kp = K + (long long)key * sg.stride_l;
         if constexpr (sizeof(T) == 2) {
@@ -281,25 +295,20 @@ __global__ void __launch_bounds__(128, WPR == 4 ? 8 : 4) cond_combine(const __gr
       l = l * corr + sum;
       m = mn;
       acc = make_float4(acc.x * corr, acc.y * corr, acc.z * corr, acc.w * corr);
-      const unsigned counts = __ballot_sync(0xffffffffu, e != 0.f);
-      const int nk = min(16, kr.n - k0);
-      for (int kb = 0; kb < nk; kb += BATCH) { // a key that does not count is not read
-        float4 x4[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) axpy4(acc, __shfl_sync(0xffffffffu, e, 2 * i), x4[i]);
+      if (counts >> 2 * BATCH) {
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
           x4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (nd > 0 && (counts >> 2 * (kb + i) & 1)) x4[i] = load4(V + (long long)(k0 + kb + i) * sg.stride_l + d0, nd);
+          if (nd > 0 && (counts >> 2 * (BATCH + i) & 1)) x4[i] = load4(vp + (BATCH + i) * sg.stride_l, nd);
         }
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) axpy4(acc, __shfl_sync(0xffffffffu, e, 2 * (kb + i)), x4[i]);
+        for (int i = 0; i < BATCH; ++i) axpy4(acc, __shfl_sync(0xffffffffu, e, 2 * (BATCH + i)), x4[i]);
       }
     }
   }
-  // the parts: sub, sub + WPR, ... (at most 64 in all)
-  const int n = p.n_split;
-  const int c0 = sub + WPR * lane, c1 = c0 + 32 * WPR;
-  const float l0 = c0 < n ? part_lse[(long long)c0 * p.part_rows + row] : -INFINITY;
-  const float l1 = c1 < n ? part_lse[(long long)c1 * p.part_rows + row] : -INFINITY;
+  // the parts
   float M = fmaxf(l0, l1) * L2E;
 #pragma unroll
   for (int y = 16; y > 0; y >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, y));
