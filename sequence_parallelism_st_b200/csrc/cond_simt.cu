@@ -23,6 +23,29 @@ __device__ __forceinline__ float4 load4(const float *p, int n, bool vec) {
   return make_float4(p[0], n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
 }
 
+// Products of the thread's 4 rows with NE of its keys (16 apart); the others of
+// a short tile hold no key.
+template <int NE>
+__device__ __forceinline__ void scores(float (&s)[4][4], const float *q, const float *k, int pitch, int DP) {
+#pragma unroll 2
+  for (int d = 0; d < DP; d += 4) {
+    float4 a[4], b[NE];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(q + i * pitch + d);
+#pragma unroll
+    for (int e = 0; e < NE; ++e) b[e] = *reinterpret_cast<const float4 *>(k + 16 * e * pitch + d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        s[i][e] = fmaf(a[i].x, b[e].x, s[i][e]);
+        s[i][e] = fmaf(a[i].y, b[e].y, s[i][e]);
+        s[i][e] = fmaf(a[i].z, b[e].z, s[i][e]);
+        s[i][e] = fmaf(a[i].w, b[e].w, s[i][e]);
+      }
+  }
+}
+
 // NC: 64-channel chunks of the head (D <= 64 * NC)
 template <int NC>
 __global__ void __launch_bounds__(NT) cond_simt_kernel(const __grid_constant__ st::CondParams p, uint32_t row_blocks, bool vec) {
@@ -101,25 +124,9 @@ __global__ void __launch_bounds__(NT) cond_simt_kernel(const __grid_constant__ s
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
-    for (int d = 0; d < DP; d += 4) {
-      float4 a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(sQ + (4 * ty + i) * PQ + d);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (16 * e < nv) b[e] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * e) * PQ + d);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (16 * e >= nv) break;               // no key of the tile's there: uniform
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[i][e] = fmaf(a[i].x, b[e].x, s[i][e]);
-          s[i][e] = fmaf(a[i].y, b[e].y, s[i][e]);
-          s[i][e] = fmaf(a[i].z, b[e].z, s[i][e]);
-          s[i][e] = fmaf(a[i].w, b[e].w, s[i][e]);
-        }
-      }
-    }
+    if (nv > BN / 2) scores<4>(s, sQ + 4 * ty * PQ, sK + tx * PQ, PQ, DP);
+    else if (nv > BN / 4) scores<2>(s, sQ + 4 * ty * PQ, sK + tx * PQ, PQ, DP);
+    else scores<1>(s, sQ + 4 * ty * PQ, sK + tx * PQ, PQ, DP);
     bool keep[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
