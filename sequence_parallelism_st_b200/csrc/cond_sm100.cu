@@ -899,9 +899,13 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
       Reader rd;
       uint32_t qc = 0, steps = 0;                      // Q tiles and steps of this tile so far
       int q0 = 0;                                      // first Q slot of the item
+      // This tile has waited for the stages it now holds (resident: those of its
+      // run).  The run's first item may have no rows for it, so a later one waits;
+      // the stages' phases stay until this tile, too, has handed them back.
+      bool landed = false;
       struct Work {                                    // what the issuer needs of an item
         int n_qt, n, n0, n1, s0, j0;
-        bool fresh, release;
+        bool release;
         // chunks of 16 keys of step j
         __device__ __forceinline__ int chunks(int j) const {
           j += j0;
@@ -919,7 +923,6 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
         wk.n1 = uniform(ip->n1);
         wk.s0 = uniform(ip->s0);
         wk.j0 = uniform(ip->j0);
-        wk.fresh = !resident || uniform(ip->fresh);
         wk.release = !resident || uniform(ip->release);
         rd.done(item_empty, lane);
         return true;
@@ -939,7 +942,7 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
             // keys as there are (whole chunks)
             const int bar = ring.bar(resident, j), st = ring.stage(a, resident, j);
             const uint32_t ph = ring.phase(resident, j);
-            if (cur.fresh && !(ok = mbar_wait(k_full + bar, ph, epoch))) break;
+            if (!landed && !(ok = mbar_wait(k_full + bar, ph, epoch))) break;
             tc_fence_after();
             const int nk = cur.chunks(j);
             const uint32_t ids = idesc_bf16(BLOCK_M, 0, 0, 0) | uint32_t(nk * 2) << 17;
@@ -957,7 +960,7 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
             tc_commit(lead, s_full + X);
             if (cur.release) tc_commit(lead, k_empty + bar);  // handed back at the last item that reads it
             // PV(j)
-            if (cur.fresh && !(ok = mbar_wait(v_ready + bar, ph, epoch))) break;
+            if (!landed && !(ok = mbar_wait(v_ready + bar, ph, epoch))) break;
             const bool last = j + inc >= cur.n;
             if (last && !(ok = fetch())) break;              // wk: now the next item
             const uint32_t va = sdesc_lo<K::VAT>(aV + st * K::VTILE);
@@ -977,7 +980,9 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
             if (cur.release) tc_commit(lead, v_empty + bar);
           }
           if (!ok) break;
+          landed = resident;
         }
+        if (cur.release) landed = false;
         // stages this tile did not use in this item: hand them back once they
         // were filled (a commit: earlier items of the run may still read them)
         if (cur.release && !spread) {
