@@ -348,6 +348,8 @@ typedef struct {
  *     O[b,t,s,h,:] = softmax_l(Q[b,t,s,h,:] . K[set(b),l,h',:] * scale) V[set(b),l,h',:]
  * over the keys l of the batch's set that count.  No such key: O = 0 and
  * lse = -inf.
+ * A score of a counted key that is NaN or +inf makes the row's O and lse NaN; one
+ * of -inf has weight 0, and a row of nothing else is a row without keys.
  *   desc: Q and O as in st_attn_spatial (their strides only; T frames of S
  *     queries, T = S = 1 for a single query); kv_begin, kv_end must be 0 and
  *     slices are not taken (ST_ERR_UNSUPPORTED).  o_fp32 writes an fp32 partial

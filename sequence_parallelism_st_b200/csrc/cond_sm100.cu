@@ -154,7 +154,8 @@ __device__ __forceinline__ float ex2_mufu(float x) {
   return y;
 }
 // 2^x on the FMA pipe for x <= 8: the degree-3 polynomial of the spatial
-// kernel (fit_exp2_poly.py; max relative error 7.5e-5), clamped at 2^-125.
+// kernel (fit_exp2_poly.py; max relative error 7.5e-5), clamped at 2^-125.  NaN
+// gives some finite number: the row's maximum carries it instead.
 constexpr float kP0 = 0.9999280571937561f, kP1 = 0.6932609677314758f;
 constexpr float kP2 = 0.2426111251115799f, kP3 = 0.0551716685295105f;
 constexpr int kPolyPairs = 2;                // of every 8 pairs of scores
@@ -187,9 +188,15 @@ __device__ __forceinline__ f32x2 fmul2(f32x2 a, f32x2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// Maxima that keep NaN (fmaxf drops it).
+__device__ __forceinline__ float fmax2(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 __device__ __forceinline__ float2 ex2_poly2(f32x2 xx) {
@@ -1145,19 +1152,22 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
         }
         float mxp[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mxp[e] = fmaxf(__uint_as_float(sr[0][2 * e]), __uint_as_float(sr[0][2 * e + 1]));
+        for (int e = 0; e < 4; ++e) mxp[e] = fmax2(__uint_as_float(sr[0][2 * e]), __uint_as_float(sr[0][2 * e + 1]));
 #pragma unroll
         for (int c = 1; c < 2 * K::CH; ++c)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             mxp[e] = fmax3(mxp[e], __uint_as_float(sr[c >> 1][(c & 1) * 8 + 2 * e]),
                            __uint_as_float(sr[c >> 1][(c & 1) * 8 + 2 * e + 1]));
-        // a step without any key leaves the row at NO_KEY: its weights are 0
-        const float mx = fmaxf(fmaxf(fmax3(mxp[0], mxp[1], mxp[2]), mxp[3]) * sl2, NO_KEY);
+        // A step without any key leaves the row at NO_KEY: its weights are 0.  A
+        // score that is NaN or +inf makes the maximum NaN (inf * 0 is NaN), and with
+        // it the weights of the row, its sum and its O, now and in later steps.
+        float mx = fmax2(fmax2(fmax3(mxp[0], mxp[1], mxp[2]), mxp[3]) * sl2, NO_KEY);
+        mx = fmaf(mx, 0.f, mx);
         if (j == first) {
           m = mx;
         } else {
-          const bool need = mx > m + 8.0f;
+          const bool need = !(mx <= m + 8.0f) && m == m;
           if (__any_sync(0xffffffffu, need)) {
             // S(j) complete means PV(j - 1) is (one thread issued both): rescale O in TMEM
             const float corr = need ? ex2_mufu(m - mx) : 1.0f;
@@ -1240,7 +1250,7 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
         tmem_wait_ld();
         l = __uint_as_float(sum[0]);
       }
-      if (some && (m > NO_KEY || l != l)) {    // else no key counted: o = 0, lse = -inf
+      if (some && m != NO_KEY) {               // else no key counted: o = 0, lse = -inf
         inv = __fdividef(1.0f, l);
         lse = (m + __log2f(l)) * 0.6931471805599453f;
       }

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import sequence_parallelism_st_b200 as st
-from test_gpu_conditioning import BF, check_attn, rand, run_cross, sets_of
+from test_gpu_conditioning import BF, F32, HEAD_DIMS, check_attn, rand, run_cross, run_prefix, sets_of
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,103 @@ def test_kept_keys_of_heads_that_share_them(D, last):
         finally:
             st.st_set_sm_budget(0)
         check_attn(q, [sets_of(k, v)], o, lse, what=f"D{D}")
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+def nan_rows(o, lse, what):
+    assert o.isnan().all() and lse.isnan().all(), what
+
+
+def finite(o, lse, what):
+    assert o.isfinite().all() and lse.isfinite().all(), what
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", HEAD_DIMS)
+@pytest.mark.parametrize("L", [1, 4, 5, 300])
+def test_values_that_are_not_finite_where_they_count(dtype, D, L):
+    """NaN in a counted key, at every place of the 16 that are weighed together, early and late; NaN in one query;
+    a score of +inf: the row's o and lse are NaN.  NaN and infinities of V reach their channel alone."""
+    S, H = 5, 2
+    q, k, v = rand(210, 1, 1, S, H, D, dtype=dtype), rand(211, 1, L, H, D, dtype=dtype), rand(212, 1, L, H, D, dtype=dtype)
+    places = sorted({i for i in list(range(16)) + [L - 1 - i for i in range(16)] if 0 <= i < L})
+    for i in places:
+        kn = k.clone()
+        kn[0, i, 0, D - 1] = NAN
+        o, lse, _ = run_cross(q, kn, v)
+        nan_rows(o[..., 0, :], lse[:, :, 0], f"K of key {i}")
+        finite(o[..., 1, :], lse[:, :, 1], f"K of key {i}, the other head")
+        vn = v.clone()
+        vn[0, i, 0, 3], vn[0, i, 0, 5], vn[0, i, 1, 7] = NAN, INF, -INF
+        o, lse, _ = run_cross(q, k, vn)
+        assert lse.isfinite().all()
+        assert o[..., 0, 3].isnan().all() and (o[..., 0, 5] == INF).all() and (o[..., 1, 7] == -INF).all()
+        rest = o.clone()
+        rest[..., 0, 3], rest[..., 0, 5], rest[..., 1, 7] = 0, 0, 0
+        assert rest.isfinite().all(), f"V of key {i}"
+        # a score beyond fp32: +inf
+        big = torch.finfo(dtype).max / 4
+        ko, qo = k.clone(), q.clone()
+        ko[0, i, 1], qo[:, :, 2, 1] = big, 8.0
+        qo[:, :, 3, 1] = -8.0                          # -inf for that key: a weight of 0, if another one counts
+        o, lse, _ = run_cross(qo, ko, v)
+        nan_rows(o[:, :, 2, 1], lse[:, :, 1, 2], f"+inf at key {i}")
+        finite(o[:, :, :, 0], lse[:, :, 0], "the other head")
+        if L > 1:
+            finite(o[:, :, 3, 1], lse[:, :, 1, 3], f"-inf at key {i}")
+        else:                                          # every score -inf: as a row without keys
+            assert not o[:, :, 3, 1].any() and (lse[:, :, 1, 3] == -INF).all()
+    for d in (0, D - 1):
+        qn = q.clone()
+        qn[0, 0, 2, 1, d] = NAN
+        o, lse, _ = run_cross(qn, k, v)
+        nan_rows(o[0, 0, 2, 1], lse[0, 0, 1, 2], "Q")
+        o[0, 0, 2, 1], lse[0, 0, 1, 2] = 0, 0
+        finite(o, lse, "the other rows")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [72, 128])
+@pytest.mark.parametrize("S", [1, 40])
+def test_values_that_are_not_finite_in_parts_and_prefixes(dtype, D, S):
+    """The same where keys are split into parts, masked between, or attended behind a prefix (own keys in the
+    combine kernel where samples are packed): one bad key that counts, in each part, makes the row NaN; one that
+    does not leaves it finite."""
+    B, H, Hkv, L = 2, 4, 2, 2000
+    q, k, v = (rand(220 + i, *s, dtype=dtype) for i, s in enumerate([(B, 1, S, H, D), (B, L, Hkv, D), (B, L, Hkv, D)]))
+    clean, clean_lse, ws = run_cross(q, k, v)
+    assert ws > 0
+    for i in (0, 5, 777, 1300, L - 1):
+        kn = k.clone()
+        kn[1, i, 1] = NAN
+        o, lse, _ = run_cross(q, kn, v)
+        nan_rows(o[1, :, :, 2:], lse[1, :, 2:], f"key {i}")
+        assert torch.equal(o[0], clean[0]) and torch.equal(o[1, :, :, :2], clean[1, :, :, :2])
+        assert torch.equal(lse[0], clean_lse[0])
+        keep = torch.ones(B, L, dtype=torch.bool)
+        keep[1, i] = False
+        o, lse, _ = run_cross(q, kn, v, kv_mask=keep.cuda())
+        finite(o, lse, "masked")
+    qn = q.clone()
+    qn[0, 0, 0, 3, 1] = NAN
+    o, lse, _ = run_cross(qn, k, v)
+    nan_rows(o[0, 0, 0, 3], lse[0, 0, 3, 0], "Q")
+    for B, sets, Lp, Lo in ((6, 2, 700, 9), (2, 2, 90, 150)):
+        q = rand(223, B, 1, S, H, D, dtype=dtype)
+        kp, vp = rand(224, sets, Lp, Hkv, D, dtype=dtype), rand(225, sets, Lp, Hkv, D, dtype=dtype)
+        ko, vo = rand(226, B, Lo, Hkv, D, dtype=dtype), rand(227, B, Lo, Hkv, D, dtype=dtype)
+        for ws in (True, False):
+            for i in (0, 3, 4, Lo - 1):
+                kn = ko.clone()
+                kn[B - 1, i, 0, 1] = NAN
+                o, lse, _ = run_prefix(q, kp, vp, kn, vo, ws=ws)
+                nan_rows(o[B - 1, :, :, :2], lse[B - 1, :, :2], f"own key {i}")
+                finite(o[:B - 1], lse[:B - 1], "the other samples")
+                kn = kp.clone()
+                kn[0, i % Lp, 1, 0] = NAN
+                o, lse, _ = run_prefix(q, kn, vp, ko, vo, ws=ws)
+                each = B // sets
+                nan_rows(o[:each, :, :, 2:], lse[:each, :, 2:], f"prefix key {i}")
+                finite(o[each:], lse[each:], "the other set")
