@@ -111,6 +111,7 @@ typedef struct {
  * attn_chunk_merge.
  *   lse: optional fp32 [B, T, H, S] dense, natural-log log-sum-exp of the
  *        scaled scores of each query row (-inf for an empty key range).
+ *   A score that is NaN or +inf makes the row's O and lse NaN.
  *   bf16 runs on the tcgen05 tensor-core kernel (fp32 accumulation); fp32 runs
  *   on an fp32 FMA kernel.  Returns ST_ERR_ALIGN if a pointer or stride is not
  *   16-byte aligned, ST_ERR_UNSUPPORTED for a bf16 head dim outside the set

@@ -173,7 +173,7 @@ __device__ __forceinline__ float ex2_mufu(float x) {
 // error over [-1/2, 1/2] (max relative error 7.5e-5, far below the bf16
 // rounding of P); 2^j is added into the exponent field.  x is clamped at -125
 // so the result stays a normal number (masked scores give 2^-125, i.e. 0 for
-// all purposes).
+// all purposes).  NaN gives some finite number too: the row's maximum carries it.
 constexpr float kP0 = 0.9999280571937561f, kP1 = 0.6932609677314758f;
 constexpr float kP2 = 0.2426111251115799f, kP3 = 0.0551716685295105f;
 
@@ -408,9 +408,15 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+// Maxima that keep NaN (fmaxf drops it).
+__device__ __forceinline__ float fmax2(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 // The polynomial 2^x of ex2_poly on a pair, with packed arithmetic.
@@ -859,11 +865,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mxp[3] = fmax3(mxp[3], __uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7]));
           }
         }
-        const float mx = fmaxf(fmax3(mxp[0], mxp[1], mxp[2]), mxp[3]) * sl2;
+        const float mx = fmax2(fmax3(mxp[0], mxp[1], mxp[2]), mxp[3]) * sl2;
+        // a NaN score makes the row's maximum NaN, and with it its weights, sum and O
+        // from here on; one of +inf stays its maximum, which the epilogue looks at
         if (j == 0) {
           m = mx;
         } else {
-          const bool need = mx > m + 8.0f;
+          const bool need = !(mx <= m + 8.0f);
           if (__any_sync(0xffffffffu, need)) {
             // O holds PV up to step gs-1: wait for it, then rescale in TMEM
             if (!(ok = mbar_wait(pv_done + 2 * X + ((gs - 1) & 1), ((gs - 1) >> 1) & 1, epoch, 15 + X))) break;
@@ -1072,7 +1080,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const float m = sStat[(X * 2 + 0) * BLOCK_M + r];
         float l = sStat[(X * 2 + 1) * BLOCK_M + r];   // replaced by O's column D with the ones column
         mbar_arrive(stat_empty + X);
-        float inv = 1.0f / l;
+        const float bad = m - m;               // NaN for a maximum of NaN or +inf, else 0
+        float inv = 1.0f / l + bad;
         float fa = 0.f, lse_row = 0.f;         // weight of the accumulated partial; LSE of the row
         const uint32_t tO = tmem + lane_off + TM_O + X * 128;
         constexpr int NCH = (D + EPI_COLS - 1) / EPI_COLS;    // 16-column chunks holding data
@@ -1090,12 +1099,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tmem_wait_ld();
           if (K::ONES && grp == 0) {           // row sum of the bf16 P, accumulated by PV
             l = __uint_as_float(ov[D / 16][D % 16]);
-            inv = 1.0f / l;
+            inv = 1.0f / l + bad;
           }
           if (grp == 0) {
             // this chunk's natural-log LSE; merged with the accumulated one when asked:
             //   w_a = exp(lse_a - M), w_c = exp(lse_c - M), o = (w_a o_a + w_c O / l) / (w_a + w_c)
-            lse_row = (m + log2f(l)) * 0.6931471805599453f;
+            lse_row = (m + log2f(l)) * 0.6931471805599453f + bad;
             if (merging) {
               const float M = fmaxf(la, lse_row);
               const float wa = expf(la - M), wc = expf(lse_row - M);
