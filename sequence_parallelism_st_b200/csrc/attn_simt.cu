@@ -61,8 +61,9 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(st::Geom g, int lo, int h
       for (int x = 16; x > 0; x >>= 1) part += __shfl_xor_sync(0xffffffffu, part, x);
       const float sc = part * scale;
       const float mn = fmaxf(m, sc);
-      const float corr = expf(m - mn);
-      const float p = expf(sc - mn);
+      const float ref = mn == -INFINITY ? 0.f : mn;    // scores of -inf alone so far: their weights are 0
+      const float corr = expf(m - ref);
+      const float p = expf(sc - ref);                  // NaN for a score of NaN or +inf
       l = l * corr + p;
 #pragma unroll
       for (int r = 0; r < MAXR; ++r) {
@@ -73,16 +74,16 @@ __global__ void __launch_bounds__(256) attn_f32_kernel(st::Geom g, int lo, int h
     }
     const long long li = TEMPORAL ? (((long long)b * g.S + sel) * g.H + h) * g.T + row
                                   : (((long long)b * g.T + sel) * g.H + h) * g.S + row;
-    float val = l > 0.f ? m + logf(l) : -INFINITY;
-    float fa = 0.f, fc = l > 0.f ? 1.f / l : 0.f;
+    float val = l == 0.f ? -INFINITY : m + logf(l);    // (l may be NaN, and is kept)
+    float fa = 0.f, fc = l == 0.f ? 0.f : 1.f / l;
     if (o_acc) {
       // merge with the accumulated partial: weights exp(lse - M) of the two
       const float la = lse_acc[li];
-      const float M = fmaxf(la, val);
+      const float M = la != la ? la : fmaxf(la, val);
       if (M != -INFINITY) {
         const float wa = expf(la - M), wc = expf(val - M), sw = wa + wc;
         fa = wa / sw;
-        fc = l > 0.f ? wc / (sw * l) : 0.f;
+        fc = l == 0.f ? 0.f : wc / (sw * l);
         val = M + logf(sw);
       }
     }

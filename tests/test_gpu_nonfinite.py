@@ -74,3 +74,39 @@ def test_spatial_few_keys(n):
     o, lse = run(st.st_attn_spatial, q, k, v, kv_begin=8, kv_end=8 + n)
     assert o[0, 0, 3].isnan().all() and lse[0, 0, 0, 3].isnan()
     assert lse.isnan().sum() == 1 and o.isnan().sum() == 72
+
+
+def test_fp32():
+    """The FMA kernel, plain, as ring and as a chain of two ranges; a first key whose score is -inf has weight 0."""
+    S = 70
+    q, k, v = (rand(320 + i, 1, 2, S, 2, 40, dtype=F32) for i in range(3))
+    places = [0, 1, 33, S - 1]
+    check_keys(lambda *x: run(st.st_attn_spatial, *x), q, k, v, places, "spatial")
+    check_keys(lambda *x: run(st.st_attn_ring, *x, 3), q, k, v, places, "ring")
+
+    def chained(q, k, v):
+        o, lse = run(st.st_attn_spatial, q, k, v, kv_begin=0, kv_end=S // 2)
+        out = torch.zeros_like(q)
+        st.st_attn_spatial_merge(q, k, v, o, lse, out, lse, kv_begin=S // 2, kv_end=S)
+        return out, lse
+    check_keys(chained, q, k, v, places, "merge")
+    # an accumulated row that is NaN stays NaN behind a range without keys and behind one with them
+    acc, lacc = run(st.st_attn_spatial, q, k, v)
+    acc[0, 0, 4, 1], lacc[0, 0, 1, 4] = NAN, NAN
+    for end in (10, 20):
+        out, lse = torch.zeros_like(q), torch.zeros_like(lacc)
+        st.st_attn_spatial_merge(q, k, v, acc, lacc, out, lse, kv_begin=10, kv_end=end)
+        assert out[0, 0, 4, 1].isnan().all() and lse[0, 0, 1, 4].isnan()
+        assert out.isnan().sum() == 40 and lse.isnan().sum() == 1
+
+
+def test_temporal():
+    for dtype, D in ((F32, 40), (BF, 72)):
+        q, k, v = (rand(330 + i, 1, 9, 6, 2, D, dtype=dtype) for i in range(3))
+        for t in range(9):
+            kn = k.clone()
+            kn[0, t, 2, 0, 1] = NAN
+            o, lse = torch.zeros_like(q), torch.zeros(1, 6, 2, 9, device="cuda")
+            st.st_attn_temporal(q, kn, v, o, lse)
+            assert o[0, :, 2, 0].isnan().all() and lse[0, 2, 0].isnan().all()
+            assert o.isnan().sum() == 9 * D and lse.isnan().sum() == 9
