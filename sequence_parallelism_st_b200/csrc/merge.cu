@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256) merge_kernel(MergeArgs a, int nc, I n_row
       float M = -INFINITY;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        if (c < n) M = fmaxf(M, l[u][c]);
+        if (c < n) M = st::max_nan(M, l[u][c]);        // a NaN chunk makes the row NaN, whatever the others hold
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       float sum = 0.f;
       if (M != -INFINITY) {

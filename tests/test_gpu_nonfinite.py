@@ -110,3 +110,23 @@ def test_temporal():
             st.st_attn_temporal(q, kn, v, o, lse)
             assert o[0, :, 2, 0].isnan().all() and lse[0, 2, 0].isnan().all()
             assert o.isnan().sum() == 9 * D and lse.isnan().sum() == 9
+
+@pytest.mark.parametrize("R", [1, 2, 3, 8])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_chunk_merge(R, dtype):
+    """A partial that is NaN makes the merged row NaN, also where the other chunks hold no key of it."""
+    U, S, H, D = 2, 33, 3, 72
+    o = [rand(340 + c, U, S, H, D, dtype=F32) for c in range(R)]
+    lse = [rand(350 + c, U, H, S, dtype=F32) for c in range(R)]
+    for c in range(R):
+        x, y = [t.clone() for t in o], [t.clone() for t in lse]
+        x[c][0, 4, 1], y[c][0, 1, 4] = NAN, NAN
+        x[c][1, 8, 2], y[c][1, 2, 8] = NAN, NAN
+        for i in range(R):
+            if i != c:
+                y[i][1, 2, 8] = -INF
+        out, lout = torch.zeros(U, S, H, D, dtype=dtype, device="cuda"), torch.zeros(U, H, S, device="cuda")
+        st.attn_chunk_merge(x, y, U, S, H, D, out, lout)
+        for u, s, h in ((0, 4, 1), (1, 8, 2)):
+            assert out[u, s, h].isnan().all() and lout[u, h, s].isnan(), (c, u)
+        assert out.isnan().sum() == 2 * D and lout.isnan().sum() == 2
