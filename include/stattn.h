@@ -381,8 +381,8 @@ size_t st_attn_cross_workspace_bytes(const st_attn_desc *desc, const st_kv_desc 
  * without laying the two behind one another.  With own->n_sets = B and the
  * samples' own tokens as queries it is in-context-conditioned (joint)
  * self-attention.  Where each sample has few queries, those that share a
- * prefix attend to it together (with a workspace), so the prefix is read once
- * for all.  Arguments, results and errors as st_attn_cross; both descriptors
+ * prefix attend to it together (with a workspace, and where their rows lie at
+ * one stride), so the prefix is read once for all.  Arguments, results and errors as st_attn_cross; both descriptors
  * may use len, offsets or mask, H_kv must be the same (ST_ERR_SHAPE). */
 st_status st_attn_prefix(const st_attn_desc *desc, const st_kv_desc *prefix, const st_kv_desc *own,
                          const void *q, const void *k_prefix, const void *v_prefix, const void *k,

@@ -112,6 +112,13 @@ st_status make_plan(const st_attn_desc *desc, const st_kv_desc *d0, const st_kv_
   }
   const long long all_rows = (long long)g.B * g.T * g.S;
   if (all_rows * g.H >= (1LL << 31) || (long long)seg0.L + (d1 ? seg1.L : 0) >= (1LL << 30)) return ST_ERR_SHAPE;
+  // One query per frame: no token stride is used, so the one between frames (or,
+  // with one frame, batches) takes its place, and queries at any distance (columns
+  // of a fused projection, say) become rows as dense ones do.
+  if (g.S == 1) {
+    const long long step = g.T > 1 ? g.st : g.sb;
+    if (step >= (long long)g.H * g.D) g.ss = step;
+  }
   p.T0 = g.T;
   p.S0 = g.S;
   p.B0 = g.B;

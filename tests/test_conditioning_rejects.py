@@ -135,3 +135,17 @@ def test_binding_checks():
 def test_qk_norm_rope_rejects_rows_beyond_its_indices():
     assert qk(h_q=(1 << 30) // 72 + 1, k=None, ko=None, h_k=0, n_tokens=1) == st.ST_ERR_SHAPE
     assert qk(h_q=2 ** 31 - 1, h_k=2 ** 31 - 1, n_tokens=1, D=8) == st.ST_ERR_SHAPE
+
+
+def test_single_queries_at_any_stride_are_rows():
+    """Queries one per sample or frame are packed whatever lies between them: the workspace of the dense layout."""
+    row = 4 * 72
+    for fn, B, kv in (("st_attn_prefix", 64, [dict(n_sets=1, L=4096), dict(n_sets=64, L=60)]),
+                      ("st_attn_cross", 64, [dict(n_sets=1, L=4096)])):
+        for desc in (dict(), dict(T=1, stride_b=3 * row), dict(stride_b=5 * row, stride_t=8, stride_s=row)):
+            assert ws_bytes(fn, dict(B=B, **desc), *kv) == ws_bytes(fn, dict(B=B), *kv) > 0, (fn, desc)
+    kv = [dict(n_sets=2, L=4096), dict(n_sets=2, L=0)]
+    dense = ws_bytes("st_attn_prefix", dict(B=2, T=30), *kv)
+    assert ws_bytes("st_attn_prefix", dict(B=2, T=30, stride_t=3 * row), *kv) == dense > 0
+    # overlapping rows are not taken for rows of a tile
+    assert ws_bytes("st_attn_prefix", dict(B=64, stride_b=8), dict(n_sets=1, L=4096), dict(n_sets=64, L=60)) == 0

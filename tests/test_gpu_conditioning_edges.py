@@ -147,3 +147,31 @@ def test_values_that_are_not_finite_in_parts_and_prefixes(dtype, D, S):
                 each = B // sets
                 nan_rows(o[:each, :, :, 2:], lse[:each, :, 2:], f"prefix key {i}")
                 finite(o[each:], lse[each:], "the other set")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H,Hkv,D", [(4, 2, 72), (2, 2, 128)])
+def test_single_queries_at_a_stride(dtype, H, Hkv, D):
+    """One query per sample, or per frame, out of rows that hold more: packed as dense ones are, with their bits,
+    and what lies between the rows stays."""
+    for B, T, sets, Lp, L in ((40, 1, 1, 900, 20), (6, 1, 2, 300, 300), (2, 25, 2, 700, 10), (1, 1, 1, 1500, 3)):
+        q = rand(230, B, T, 1, H, D, dtype=dtype)
+        wide = rand(231, B, T, 1, 3 * H, D, dtype=dtype)
+        wide[..., :H, :] = q
+        out, lse = torch.full_like(wide, 7.0), torch.empty(B, T, H, 1, device="cuda")
+        kp, vp = rand(232, sets, Lp, Hkv, D, dtype=dtype), rand(233, sets, Lp, Hkv, D, dtype=dtype)
+        k, v = rand(234, B, L, Hkv, D, dtype=dtype), rand(235, B, L, Hkv, D, dtype=dtype)
+        for kw in (dict(), dict(kv_len=torch.arange(B, dtype=torch.int32).remainder(L + 1).cuda())):
+            segs = [sets_of(kp, vp), sets_of(k, v, kw.get("kv_len"))]
+            o, l, n = run_prefix(q, kp, vp, k, v, **kw)
+            check_attn(q, segs, o, l, what="dense")
+            assert st.st_attn_prefix_workspace_bytes(wide[..., :H, :], kp, k, **kw) == n
+            for ws in (None, torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")):
+                st.st_attn_prefix(wide[..., :H, :], kp, vp, k, v, out[..., :H, :], lse, workspace=ws, **kw)
+                check_attn(q, segs, out[..., :H, :], lse, what="strided")
+            assert torch.equal(out[..., :H, :], o) and torch.equal(lse, l)
+        o, l, n = run_cross(q, kp, vp)
+        assert st.st_attn_cross_workspace_bytes(wide[..., :H, :], kp) == n
+        st.st_attn_cross(wide[..., :H, :], kp, vp, out[..., :H, :], lse, workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
+        assert torch.equal(out[..., :H, :], o) and torch.equal(lse, l)
+        assert (out[..., H:, :] == 7.0).all()
