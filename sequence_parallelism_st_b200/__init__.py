@@ -503,8 +503,7 @@ def _kv_desc(where, head_dim, q, k, v, length, offsets, mask, max_len):
         if length is not None or mask is not None:
             raise StattnError(ST_ERR_SHAPE, f"{where}: offsets exclude lengths and mask")
         d.n_sets, d.n_rows = offsets.numel() - 1, L
-        if max_len is not None:
-            d.L = int(max_len)
+        d.L = max(L, 1) if max_len is None else int(max_len)     # (no rows at all: sets without keys)
         d.offsets = _int32(where, offsets, d.n_sets + 1, index)
         return d
     n = size[0]

@@ -149,3 +149,15 @@ def test_single_queries_at_any_stride_are_rows():
     assert ws_bytes("st_attn_prefix", dict(B=2, T=30, stride_t=3 * row), *kv) == dense > 0
     # overlapping rows are not taken for rows of a tile
     assert ws_bytes("st_attn_prefix", dict(B=64, stride_b=8), dict(n_sets=1, L=4096), dict(n_sets=64, L=60)) == 0
+
+
+def test_binding_takes_packed_sets_of_no_rows():
+    """Offsets over K of no rows describe sets without keys, with and without max_len (not a descriptor of L = 0)."""
+    q, k = torch.zeros(2, 1, 3, 4, 8), torch.zeros(0, 2, 8)
+    off = torch.zeros(3, dtype=torch.int32)
+    for most in (None, 7):
+        d = st._kv_desc("test", 8, q, k, k, None, off, None, most)
+        assert d.L >= 1 and d.n_rows == 0 and d.n_sets == 2
+        a = st.make_desc(2, 1, 3, 4, 8, st.ST_F32)
+        assert st._c["st_attn_cross"](ctypes.byref(a), ctypes.byref(d), VP(Q.value + 2), None, None, O, None, None, 0,
+                                      None) == st.ST_ERR_ALIGN       # (past the checks of the descriptor)

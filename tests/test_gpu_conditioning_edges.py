@@ -175,3 +175,19 @@ def test_single_queries_at_a_stride(dtype, H, Hkv, D):
         st.st_attn_cross(wide[..., :H, :], kp, vp, out[..., :H, :], lse, workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
         assert torch.equal(out[..., :H, :], o) and torch.equal(lse, l)
         assert (out[..., H:, :] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("max_len", [None, 5])
+def test_packed_sets_of_no_rows(dtype, max_len):
+    """Every prompt empty: K and V of no rows, with offsets: o = 0, lse = -inf, and nothing beside a prefix."""
+    B, S, H, D = 3, 6, 2, 72
+    q = rand(240, B, 1, S, H, D, dtype=dtype)
+    e = torch.empty(0, H, D, dtype=dtype, device="cuda")
+    off = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    o, lse, _ = run_cross(q, e, e, kv_offsets=off, max_len=max_len)
+    assert not o.any() and (lse == -INF).all()
+    kp, vp = rand(241, 1, 70, H, D, dtype=dtype), rand(242, 1, 70, H, D, dtype=dtype)
+    for ws in (True, False):
+        o, lse, _ = run_prefix(q, kp, vp, e, e, ws=ws, kv_offsets=off, max_len=max_len)
+        check_attn(q, [sets_of(kp, vp)], o, lse, what="no own keys")
