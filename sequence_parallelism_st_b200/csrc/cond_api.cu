@@ -382,9 +382,13 @@ __global__ void __launch_bounds__(128, WPR == 4 && sizeof(T) == 2 ? 8 : 4) cond_
   if (p.lse && lane == 0) p.lse[st::cond_lse(p, unit, w, r)] = sum == 0.f ? -INFINITY : (M + log2f(sum)) / L2E;
 }
 
-// Four warps per row while that many blocks run at once (8 fit an SM), else a
-// warp.  Whole calls, four warps and one: 1024 rows of 27 parts and 64 own keys
-// 51.8 and 56.8 us, 2048 rows of 12 parts and 64 own keys 50.7 and 36.2.
+// Four warps per row up to 8 rows per SM, else a warp.  So many bf16 blocks run at
+// once; of fp32 4 fit an SM with own keys and 7 without, and their second round
+// still pays.  Whole calls behind one prefix, 64 own keys, four warps and one: bf16,
+// 72 channels, 1024 rows of 27 parts 47.6 and 54.0 us from HBM (37.2 and 35.0 where
+// all of it stays in L2), 2048 rows of 12 parts 50.7 and 36.2; fp32, 592 rows of 16
+// parts 90 and 113, 1024 rows 104 and 117 (128 channels 141 and 164), 1536 rows of 9
+// parts 193 both.
 template <typename T, bool OWN> st_status combine_own(const CondParams &p, cudaStream_t s) {
   if (p.part_rows <= (long long)st::device_sms() * 8)
     return st::launch_pdl(cond_combine<T, OWN, 4>, dim3(unsigned(p.part_rows)), dim3(128), 0, s, p);
