@@ -350,11 +350,15 @@ def ulysses_relayout_rope(mode, inp, out, P, B, T_or_N, S_or_H, C_or_D, n_t=1, n
 
 
 # ---------------------------------------------------------------- conditioning
+def _on_gpu(where, device):
+    if device.type != "cuda":
+        raise StattnError(ST_ERR_NULL, f"{where}: tensors must be on a CUDA device")
+
+
 def _device_call(where, fn, device, stream, *args):
     """fn(*args, stream) with ``device`` current, on ``stream`` or the device's current stream."""
     import torch
-    if device.type != "cuda":
-        raise StattnError(ST_ERR_NULL, f"{where}: tensors must be on a CUDA device")
+    _on_gpu(where, device)
     # (the raw handle: a Stream object costs 3 us a call)
     s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
     if device.index == torch.cuda.current_device():
@@ -566,6 +570,7 @@ def st_attn_cross_workspace_bytes(q, k, *, kv_len=None, kv_offsets=None, kv_mask
     """Bytes of workspace st_attn_cross asks for with these arguments (0: none)."""
     desc = desc if desc is not None else _q_desc("st_attn_cross_workspace_bytes", q, None, kw)
     kv = _kv_desc("st_attn_cross_workspace_bytes", desc.D, q, k, None, kv_len, kv_offsets, kv_mask, max_len)
+    _on_gpu("st_attn_cross_workspace_bytes", q.device)
     import torch
     with torch.cuda.device(q.device):
         return int(_c["st_attn_cross_workspace_bytes"](ctypes.byref(desc), ctypes.byref(kv)))
@@ -596,6 +601,7 @@ def st_attn_prefix_workspace_bytes(q, k_prefix, k, *, prefix_len=None, prefix_of
     desc = desc if desc is not None else _q_desc(where, q, None, kw)
     pre = _kv_desc(where, desc.D, q, k_prefix, None, prefix_len, prefix_offsets, prefix_mask, prefix_max_len)
     kv = _kv_desc(where, desc.D, q, k, None, kv_len, kv_offsets, kv_mask, max_len)
+    _on_gpu(where, q.device)
     import torch
     with torch.cuda.device(q.device):
         return int(_c["st_attn_prefix_workspace_bytes"](ctypes.byref(desc), ctypes.byref(pre), ctypes.byref(kv)))

@@ -161,3 +161,11 @@ def test_binding_takes_packed_sets_of_no_rows():
         a = st.make_desc(2, 1, 3, 4, 8, st.ST_F32)
         assert st._c["st_attn_cross"](ctypes.byref(a), ctypes.byref(d), VP(Q.value + 2), None, None, O, None, None, 0,
                                       None) == st.ST_ERR_ALIGN       # (past the checks of the descriptor)
+
+
+def test_workspace_bytes_of_tensors_off_the_gpu():
+    q, k = torch.zeros(2, 1, 3, 4, 8), torch.zeros(2, 5, 2, 8)
+    for call in (lambda: st.st_attn_cross_workspace_bytes(q, k), lambda: st.st_attn_prefix_workspace_bytes(q, k, k)):
+        with pytest.raises(st.StattnError) as e:
+            call()
+        assert e.value.code == st.ST_ERR_NULL
