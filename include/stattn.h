@@ -352,8 +352,9 @@ typedef struct {
  * A score of a counted key that is NaN or +inf makes the row's O and lse NaN; one
  * of -inf has weight 0, and a row of nothing else is a row without keys.
  *   desc: Q and O as in st_attn_spatial (their strides only; T frames of S
- *     queries, T = S = 1 for a single query); kv_begin, kv_end must be 0 and
- *     slices are not taken (ST_ERR_UNSUPPORTED).  o_fp32 writes an fp32 partial
+ *     queries, T = S = 1 for a single query; bf16 takes tokens at one stride and
+ *     batches of whole frame blocks, fp32 the two-level strides too); kv_begin,
+ *     kv_end must be 0 and slices are not taken (ST_ERR_UNSUPPORTED).  o_fp32 writes an fp32 partial
  *     that st_attn_spatial_merge and attn_chunk_merge take with its lse.
  *   lse: optional fp32 [B, T, H, S] dense.
  *   workspace: device memory of st_attn_cross_workspace_bytes bytes, 16-byte

@@ -89,11 +89,14 @@ struct CondParams {
 __host__ __device__ __forceinline__ int cond_units(const CondParams &p) { return p.g.B * p.g.T; }
 // First batch of a unit.
 __device__ __forceinline__ int cond_batch(const CondParams &p, int unit) { return unit / p.g.T * p.bm; }
-// Packed row r of walked head w: element offset in Q and O.
+// Packed row r of walked head w: element offset in Q and O.  BLOCKS: tokens may
+// lie at a two-level stride (fp32; the tensor maps of bf16 take one).
+template <bool BLOCKS>
 __device__ __forceinline__ long long cond_row(const CondParams &p, int unit, int w, int r) {
   const int s = r / p.G, g = r - s * p.G;
   const int b = unit / p.g.T, t = unit - b * p.g.T;
-  return p.g.frame(b, t) + (long long)s * p.g.ss + (long long)(w * p.G + g) * p.g.D;
+  const long long token = BLOCKS ? p.g.token(s) : (long long)s * p.g.ss;
+  return p.g.frame(b, t) + token + (long long)(w * p.G + g) * p.g.D;
 }
 // Its index in the caller's LSE [B, T, H, S].
 __device__ __forceinline__ long long cond_lse(const CondParams &p, int unit, int w, int r) {

@@ -91,8 +91,11 @@ st_status make_plan(const st_attn_desc *desc, const st_kv_desc *d0, const st_kv_
   if (lo != 0 || hi != g.T) return ST_ERR_UNSUPPORTED;
   const bool bf16 = desc->dtype == ST_BF16;
   if (bf16 ? !d_supported(g.D) : g.D > 128) return ST_ERR_UNSUPPORTED;
-  if (g.sblk != g.S && g.ssb != (long long)g.sblk * g.ss) return ST_ERR_UNSUPPORTED;
-  if (g.tblk != g.T && g.sb != (long long)(g.T / g.tblk) * g.stb) return ST_ERR_UNSUPPORTED;
+  // the tensor maps take tokens at one stride and batches of whole frame blocks
+  // (as st_attn_spatial); the fp32 kernel finds each row by itself
+  const bool tokens = g.sblk == g.S || g.ssb == (long long)g.sblk * g.ss;
+  if (bf16 && !tokens) return ST_ERR_UNSUPPORTED;
+  if (bf16 && g.tblk != g.T && g.sb != (long long)(g.T / g.tblk) * g.stb) return ST_ERR_UNSUPPORTED;
   if (g.ss < (long long)g.H * g.D) return ST_ERR_SHAPE;
   if (bf16 && (g.ss % 8 || g.st % 8 || g.stb % 8 || g.sb % 8)) return ST_ERR_ALIGN;
   CondParams &p = pl.p;
@@ -124,13 +127,16 @@ st_status make_plan(const st_attn_desc *desc, const st_kv_desc *d0, const st_kv_
   p.B0 = g.B;
   p.bm = 1;
   // one stride between all rows of a batch
-  const bool flat = g.T == 1 || (g.st == (long long)g.S * g.ss && (g.tblk == g.T || g.stb == (long long)g.tblk * g.st));
+  const bool flat = tokens && (g.T == 1 || (g.st == (long long)g.S * g.ss &&
+                                            (g.tblk == g.T || g.stb == (long long)g.tblk * g.st)));
   if (flat) {
     g.S *= g.T;
     g.T = 1;
   }
-  g.sblk = g.S;
-  g.ssb = (long long)g.S * g.ss;
+  if (tokens) {
+    g.sblk = g.S;
+    g.ssb = (long long)g.S * g.ss;
+  }
   if (flat) {
     g.tblk = 1;
     g.st = g.stb = g.ssb;
@@ -226,7 +232,7 @@ __global__ void __launch_bounds__(128, WPR == 4 && sizeof(T) == 2 ? 8 : 4) cond_
   if (row >= p.part_rows) return;              // (WPR = 4: a block per row, none past the last)
   const uint32_t col = row / uint32_t(p.R);
   const int r = int(row - col * uint32_t(p.R)), unit = int(col / uint32_t(p.HW)), w = int(col) - unit * p.HW;
-  const long long off = st::cond_row(p, unit, w, r);
+  const long long off = st::cond_row<sizeof(T) == 4>(p, unit, w, r);
   const float *part_lse = st::after_wait(p.part_lse), *part_o = st::after_wait(p.part_o);
   // the parts of this warp: sub, sub + WPR, ... (at most 64 in all)
   const int n = p.n_split;

@@ -1239,7 +1239,7 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
         const long long prow = (long long)part * a.c.part_rows + ((long long)it.unit * a.c.HW + it.w) * a.c.R + row;
         f32 = a.c.part_o || a.c.o_f32;
         out = a.c.part_o ? reinterpret_cast<char *>(a.c.part_o + prow * D)
-                         : static_cast<char *>(a.c.o) + st::cond_row(a.c, it.unit, it.w, row) * (f32 ? 4 : 2);
+                         : static_cast<char *>(a.c.o) + st::cond_row<false>(a.c, it.unit, it.w, row) * (f32 ? 4 : 2);
       }
       // O leaves TMEM in groups of chunks of 16 columns, from the last ones
       // (which may hold the row sum)

@@ -169,3 +169,13 @@ def test_workspace_bytes_of_tensors_off_the_gpu():
         with pytest.raises(st.StattnError) as e:
             call()
         assert e.value.code == st.ST_ERR_NULL
+
+
+@pytest.mark.parametrize("fn", ["st_attn_cross", "st_attn_prefix"])
+def test_two_level_strides_are_taken_in_fp32(fn):
+    """Token blocks and frame blocks of the sliced layouts: fp32 goes on to the next check, bf16 is refused."""
+    row = 4 * 72
+    for desc in (dict(s_block=8, stride_sb=8 * row + 8, stride_t=1 << 20),
+                 dict(t_block=1, stride_tb=1 << 22, stride_b=1 << 16)):
+        assert cross(fn, q=VP(Q.value + 2), desc=dict(desc, dtype=st.ST_F32)) == st.ST_ERR_ALIGN
+        assert cross(fn, desc=desc) == st.ST_ERR_UNSUPPORTED

@@ -191,3 +191,30 @@ def test_packed_sets_of_no_rows(dtype, max_len):
     for ws in (True, False):
         o, lse, _ = run_prefix(q, kp, vp, e, e, ws=ws, kv_offsets=off, max_len=max_len)
         check_attn(q, [sets_of(kp, vp)], o, lse, what="no own keys")
+
+
+@pytest.mark.parametrize("S,L,Lp", [(40, 33, 70), (2, 1500, 900), (130, 64, 1)])
+@pytest.mark.parametrize("D", [72, 30])
+def test_fp32_two_level_strides(S, L, Lp, D):
+    """The sliced layout [token block, frame block, batch, frame, token, C] with gaps: Q and O found row by row, what
+    lies between them left as it was."""
+    B, T, H = 2, 4, 2
+    nt, ns = 2, 2
+    C, tf, ts = H * D, T // nt, S // ns
+    big = rand(250, ns, nt, B, tf, ts + 3, C + 5, dtype=F32)
+    dim = dict(zip(("ns", "nt", "b", "tf", "ts", "c"), big.stride()))
+    desc = st.make_desc(B, T, S, H, D, st.ST_F32, stride_b=dim["b"], stride_t=dim["tf"], t_block=tf,
+                        stride_tb=dim["nt"], stride_s=dim["ts"], s_block=ts, stride_sb=dim["ns"])
+
+    def logical(x):
+        return x[:, :, :, :, :ts, :C].permute(2, 1, 3, 0, 4, 5).reshape(B, T, S, H, D)
+    k, v, kp, vp = (rand(251 + i, B if i < 2 else 1, n, H, D, dtype=F32) for i, n in enumerate((L, L, Lp, Lp)))
+    q = logical(big)
+    for fn, keys, segs in ((st.st_attn_cross, (k, v), [sets_of(k, v)]),
+                           (st.st_attn_prefix, (kp, vp, k, v), [sets_of(kp, vp), sets_of(k, v)])):
+        n = getattr(st, fn.__name__ + "_workspace_bytes")(big, *keys[::2], desc=desc)
+        for ws in (None, torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")):
+            out, lse = torch.full_like(big, 7.0), torch.full((B, T, H, S), NAN, device="cuda")
+            fn(big, *keys, out, lse, workspace=ws, desc=desc)
+            check_attn(q, segs, logical(out), lse, what=fn.__name__)
+            assert (out[..., ts:, :] == 7.0).all() and (out[..., C:] == 7.0).all()
