@@ -218,7 +218,9 @@ __device__ __forceinline__ void axpy4(float4 &a, float w, const float4 &x) {
 
 constexpr int BATCH = 8;       // loads of a lane in flight
 
-template <typename T, bool OWN, int WPR>
+// LOOP: a block takes row after row (under a budget; with the loop the bf16 kernel
+// spills, one token behind a prefix 54 for 48 us).
+template <typename T, bool OWN, int WPR, bool LOOP>
 __global__ void __launch_bounds__(128, WPR == 4 && sizeof(T) == 2 ? 8 : 4) cond_combine(const __grid_constant__ CondParams p) {
   __shared__ __align__(16) float sq[4][128];
   __shared__ float sm[4], sl[4];
@@ -228,164 +230,171 @@ __global__ void __launch_bounds__(128, WPR == 4 && sizeof(T) == 2 ? 8 : 4) cond_
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
   const int sub = wp % WPR;                    // this warp's share of the row
   const int D = p.g.D, d0 = 4 * lane, nd = D - d0;
-  const uint32_t row = blockIdx.x * (4 / WPR) + wp / WPR;    // (rows of a call: below 2^31)
-  if (row >= p.part_rows) return;              // (WPR = 4: a block per row, none past the last)
-  const uint32_t col = row / uint32_t(p.R);
-  const int r = int(row - col * uint32_t(p.R)), unit = int(col / uint32_t(p.HW)), w = int(col) - unit * p.HW;
-  const long long off = st::cond_row<sizeof(T) == 4>(p, unit, w, r);
-  const float *part_lse = st::after_wait(p.part_lse), *part_o = st::after_wait(p.part_o);
-  // the parts of this warp: sub, sub + WPR, ... (at most 64 in all)
-  const int n = p.n_split;
-  const int c0 = sub + WPR * lane, c1 = c0 + 32 * WPR;
-  const float l0 = c0 < n ? part_lse[(long long)c0 * p.part_rows + row] : -INFINITY;
-  const float l1 = c1 < n ? part_lse[(long long)c1 * p.part_rows + row] : -INFINITY;
-  float m = -INFINITY, l = 0.f;                // running max (log2 units) and sum; the same in all lanes
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if constexpr (OWN) {
-    const T *q = static_cast<const T *>(st::after_wait(p.q)) + off;
-    const float sl2 = p.scale * L2E;
-    if (nd > 0) {
-      const float4 x = load4(q + d0, nd);
-      *reinterpret_cast<float4 *>(&sq[wp][d0]) = make_float4(x.x * sl2, x.y * sl2, x.z * sl2, x.w * sl2);
-    }
-    __syncwarp();
-    const int b = cond_batch(p, unit) + r / p.G / (p.T0 * p.S0);
-    st::KvSeg sg = p.own;
-    sg.len = st::after_wait(sg.len);
-    sg.offsets = st::after_wait(sg.offsets);
-    const st::KvRange kr = st::kv_range(sg, b);
-    const long long base = (long long)kr.set * (sg.offsets ? 0 : sg.stride_set) + (long long)kr.row0 * sg.stride_l +
-                           (long long)((w * p.G + r % p.G) / (p.G * p.hdiv)) * D;
-    const T *K = static_cast<const T *>(st::after_wait(sg.k)) + base;
-    const T *V = static_cast<const T *>(st::after_wait(sg.v)) + base;
-    const unsigned char *mk = sg.mask ? st::after_wait(sg.mask) + (long long)kr.set * sg.L : nullptr;
-    for (int k0 = 16 * sub; k0 < kr.n; k0 += 16 * WPR) {
-      const int key = k0 + (lane >> 1), half = lane & 1;     // two lanes per key, every other 8 channels each
-      float x = 0.f;
-      const bool on = key < kr.n && (!mk || mk[key]);
-      // V of the first keys is on its way with K (a key that does not count is not read)
-      const unsigned counts = __ballot_sync(0xffffffffu, on);
-      const T *vp = V + (long long)k0 * sg.stride_l + d0;
-      float4 x4[BATCH];
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        x4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (nd > 0 && (counts >> 2 * i & 1)) x4[i] = load4(vp + i * sg.stride_l, nd);
+  // (rows of a call: below 2^31; WPR = 4: the rows of a block's warps are the same)
+#pragma unroll 1
+  for (uint32_t row = blockIdx.x * (4 / WPR) + wp / WPR; row < p.part_rows; row += gridDim.x * (4 / WPR)) {
+    const uint32_t col = row / uint32_t(p.R);
+    const int r = int(row - col * uint32_t(p.R)), unit = int(col / uint32_t(p.HW)), w = int(col) - unit * p.HW;
+    const long long off = st::cond_row<sizeof(T) == 4>(p, unit, w, r);
+    const float *part_lse = st::after_wait(p.part_lse), *part_o = st::after_wait(p.part_o);
+    // the parts of this warp: sub, sub + WPR, ... (at most 64 in all)
+    const int n = p.n_split;
+    const int c0 = sub + WPR * lane, c1 = c0 + 32 * WPR;
+    const float l0 = c0 < n ? part_lse[(long long)c0 * p.part_rows + row] : -INFINITY;
+    const float l1 = c1 < n ? part_lse[(long long)c1 * p.part_rows + row] : -INFINITY;
+    float m = -INFINITY, l = 0.f;                // running max (log2 units) and sum; the same in all lanes
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (OWN) {
+      const T *q = static_cast<const T *>(st::after_wait(p.q)) + off;
+      const float sl2 = p.scale * L2E;
+      if (nd > 0) {
+        const float4 x = load4(q + d0, nd);
+        *reinterpret_cast<float4 *>(&sq[wp][d0]) = make_float4(x.x * sl2, x.y * sl2, x.z * sl2, x.w * sl2);
       }
-      if (on) {
-        const T *kp = K + (long long)key * sg.stride_l;
-        if constexpr (sizeof(T) == 2) {
-          uint4 v[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            if (16 * c + 8 * half < D) v[c] = *reinterpret_cast<const uint4 *>(kp + 16 * c + 8 * half);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const int d = 16 * c + 8 * half;
-            if (d >= D) break;
-            const uint32_t u[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x = fmaf(sq[wp][d + 2 * i], __uint_as_float(u[i] << 16), x);
-              x = fmaf(sq[wp][d + 2 * i + 1], __uint_as_float(u[i] & 0xffff0000u), x);
-            }
-          }
-        } else {
-#pragma unroll 8
-          for (int d = half; d < D; d += 2) x = fmaf(sq[wp][d], kp[d], x);
-        }
-      }
-      x += __shfl_xor_sync(0xffffffffu, x, 1);
-      if (!on) x = -INFINITY;
-      float mx = x;
-#pragma unroll
-      for (int y = 16; y > 0; y >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
-      const float mn = fmaxf(m, mx);
-      const float ref = mn == -INFINITY ? 0.f : mn;
-      const float corr = exp2f(m - ref), e = exp2f(x - ref);
-      float sum = e;
-#pragma unroll
-      for (int y = 16; y > 1; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
-      l = l * corr + sum;
-      m = mn;
-      acc = make_float4(acc.x * corr, acc.y * corr, acc.z * corr, acc.w * corr);
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) axpy4(acc, __shfl_sync(0xffffffffu, e, 2 * i), x4[i]);
-      if (counts >> 2 * BATCH) {
+      __syncwarp();
+      const int b = cond_batch(p, unit) + r / p.G / (p.T0 * p.S0);
+      st::KvSeg sg = p.own;
+      sg.len = st::after_wait(sg.len);
+      sg.offsets = st::after_wait(sg.offsets);
+      const st::KvRange kr = st::kv_range(sg, b);
+      const long long base = (long long)kr.set * (sg.offsets ? 0 : sg.stride_set) + (long long)kr.row0 * sg.stride_l +
+                             (long long)((w * p.G + r % p.G) / (p.G * p.hdiv)) * D;
+      const T *K = static_cast<const T *>(st::after_wait(sg.k)) + base;
+      const T *V = static_cast<const T *>(st::after_wait(sg.v)) + base;
+      const unsigned char *mk = sg.mask ? st::after_wait(sg.mask) + (long long)kr.set * sg.L : nullptr;
+      for (int k0 = 16 * sub; k0 < kr.n; k0 += 16 * WPR) {
+        const int key = k0 + (lane >> 1), half = lane & 1;     // two lanes per key, every other 8 channels each
+        float x = 0.f;
+        const bool on = key < kr.n && (!mk || mk[key]);
+        // V of the first keys is on its way with K (a key that does not count is not read)
+        const unsigned counts = __ballot_sync(0xffffffffu, on);
+        const T *vp = V + (long long)k0 * sg.stride_l + d0;
+        float4 x4[BATCH];
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
           x4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (nd > 0 && (counts >> 2 * (BATCH + i) & 1)) x4[i] = load4(vp + (BATCH + i) * sg.stride_l, nd);
+          if (nd > 0 && (counts >> 2 * i & 1)) x4[i] = load4(vp + i * sg.stride_l, nd);
         }
+        if (on) {
+          const T *kp = K + (long long)key * sg.stride_l;
+          if constexpr (sizeof(T) == 2) {
+            uint4 v[8];
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) axpy4(acc, __shfl_sync(0xffffffffu, e, 2 * (BATCH + i)), x4[i]);
+            for (int c = 0; c < 8; ++c)
+              if (16 * c + 8 * half < D) v[c] = *reinterpret_cast<const uint4 *>(kp + 16 * c + 8 * half);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const int d = 16 * c + 8 * half;
+              if (d >= D) break;
+              const uint32_t u[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                x = fmaf(sq[wp][d + 2 * i], __uint_as_float(u[i] << 16), x);
+                x = fmaf(sq[wp][d + 2 * i + 1], __uint_as_float(u[i] & 0xffff0000u), x);
+              }
+            }
+          } else {
+#pragma unroll 8
+            for (int d = half; d < D; d += 2) x = fmaf(sq[wp][d], kp[d], x);
+          }
+        }
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        if (!on) x = -INFINITY;
+        float mx = x;
+#pragma unroll
+        for (int y = 16; y > 0; y >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+        const float mn = fmaxf(m, mx);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float corr = exp2f(m - ref), e = exp2f(x - ref);
+        float sum = e;
+#pragma unroll
+        for (int y = 16; y > 1; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+        l = l * corr + sum;
+        m = mn;
+        acc = make_float4(acc.x * corr, acc.y * corr, acc.z * corr, acc.w * corr);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) axpy4(acc, __shfl_sync(0xffffffffu, e, 2 * i), x4[i]);
+        if (counts >> 2 * BATCH) {
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            x4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (nd > 0 && (counts >> 2 * (BATCH + i) & 1)) x4[i] = load4(vp + (BATCH + i) * sg.stride_l, nd);
+          }
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) axpy4(acc, __shfl_sync(0xffffffffu, e, 2 * (BATCH + i)), x4[i]);
+        }
       }
     }
-  }
-  // the parts
-  float M = fmaxf(l0, l1) * L2E;
+    // the parts
+    float M = fmaxf(l0, l1) * L2E;
 #pragma unroll
-  for (int y = 16; y > 0; y >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, y));
-  M = fmaxf(M, m);
-  const float ref = M == -INFINITY ? 0.f : M;
-  const float own = exp2f(m - ref);            // 0 without own keys
-  const float w0 = exp2f(l0 * L2E - ref), w1 = exp2f(l1 * L2E - ref);
-  float sum = w0 + w1;
+    for (int y = 16; y > 0; y >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, y));
+    M = fmaxf(M, m);
+    const float ref = M == -INFINITY ? 0.f : M;
+    const float own = exp2f(m - ref);            // 0 without own keys
+    const float w0 = exp2f(l0 * L2E - ref), w1 = exp2f(l1 * L2E - ref);
+    float sum = w0 + w1;
 #pragma unroll
-  for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
-  sum += l * own;
-  acc = make_float4(acc.x * own, acc.y * own, acc.z * own, acc.w * own);
-  for (int b = 0; sub + WPR * b < n; b += BATCH) {
-    float4 x4[BATCH];
-    float wc[BATCH];
+    for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+    sum += l * own;
+    acc = make_float4(acc.x * own, acc.y * own, acc.z * own, acc.w * own);
+    for (int b = 0; sub + WPR * b < n; b += BATCH) {
+      float4 x4[BATCH];
+      float wc[BATCH];
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int c = b + i;                     // (c <= 63; a part past the last has weight 0)
-      wc[i] = __shfl_sync(0xffffffffu, c < 32 ? w0 : w1, c & 31);
-      x4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (wc[i] != 0.f && nd > 0) {
-        const float *src = part_o + ((long long)(sub + WPR * c) * p.part_rows + row) * D + d0;
-        if constexpr (sizeof(T) == 2) x4[i] = *reinterpret_cast<const float4 *>(src);
-        else x4[i] = load4(src, nd);
+      for (int i = 0; i < BATCH; ++i) {
+        const int c = b + i;                     // (c <= 63; a part past the last has weight 0)
+        wc[i] = __shfl_sync(0xffffffffu, c < 32 ? w0 : w1, c & 31);
+        x4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (wc[i] != 0.f && nd > 0) {
+          const float *src = part_o + ((long long)(sub + WPR * c) * p.part_rows + row) * D + d0;
+          if constexpr (sizeof(T) == 2) x4[i] = *reinterpret_cast<const float4 *>(src);
+          else x4[i] = load4(src, nd);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) axpy4(acc, wc[i], x4[i]);
+    }
+    if constexpr (WPR > 1) {                     // join the warps of the row
+      if (lane == 0) {
+        sm[wp] = M;
+        sl[wp] = sum;
+      }
+      __syncthreads();
+      const float all = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+      const float base = all == -INFINITY ? 0.f : all;
+      const float scale = exp2f(M - base);       // 0 for a warp without a key
+      *reinterpret_cast<float4 *>(&sq[wp][d0]) = make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum = fmaf(sl[i], exp2f(sm[i] - base), sum);
+      M = all;
+      __syncthreads();
+      if (!LOOP && sub) return;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) axpy4(acc, 1.f, *reinterpret_cast<const float4 *>(&sq[i][d0]));
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+    if (sub == 0 && nd > 0) {
+      if (p.o_f32) {
+        float *o = static_cast<float *>(p.o) + off + d0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < nd) o[i] = y[i];
+      } else {
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + off + d0) =
+            make_uint2(st::pack_bf16x2(y[0], y[1]), st::pack_bf16x2(y[2], y[3]));
       }
     }
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) axpy4(acc, wc[i], x4[i]);
+    if (sub == 0 && p.lse && lane == 0)
+      p.lse[st::cond_lse(p, unit, w, r)] = sum == 0.f ? -INFINITY : (M + log2f(sum)) / L2E;
+    if constexpr (!LOOP) return;
+    // the next row's Q goes where this one's sums (WPR > 1) or Q are still read
+    if constexpr (WPR > 1) __syncthreads();
+    else __syncwarp();
   }
-  if constexpr (WPR > 1) {                     // join the warps of the row
-    if (lane == 0) {
-      sm[wp] = M;
-      sl[wp] = sum;
-    }
-    __syncthreads();
-    const float all = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    const float base = all == -INFINITY ? 0.f : all;
-    const float scale = exp2f(M - base);       // 0 for a warp without a key
-    *reinterpret_cast<float4 *>(&sq[wp][d0]) = make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
-    sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum = fmaf(sl[i], exp2f(sm[i] - base), sum);
-    M = all;
-    __syncthreads();
-    if (sub) return;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) axpy4(acc, 1.f, *reinterpret_cast<const float4 *>(&sq[i][d0]));
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-  if (nd > 0) {
-    if (p.o_f32) {
-      float *o = static_cast<float *>(p.o) + off + d0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < nd) o[i] = y[i];
-    } else {
-      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + off + d0) =
-          make_uint2(st::pack_bf16x2(y[0], y[1]), st::pack_bf16x2(y[2], y[3]));
-    }
-  }
-  if (p.lse && lane == 0) p.lse[st::cond_lse(p, unit, w, r)] = sum == 0.f ? -INFINITY : (M + log2f(sum)) / L2E;
 }
 
 // Four warps per row up to 8 rows per SM, else a warp.  So many bf16 blocks run at
@@ -396,9 +405,15 @@ __global__ void __launch_bounds__(128, WPR == 4 && sizeof(T) == 2 ? 8 : 4) cond_
 // parts 90 and 113, 1024 rows 104 and 117 (128 channels 141 and 164), 1536 rows of 9
 // parts 193 both.
 template <typename T, bool OWN> st_status combine_own(const CondParams &p, cudaStream_t s) {
-  if (p.part_rows <= (long long)st::device_sms() * 8)
-    return st::launch_pdl(cond_combine<T, OWN, 4>, dim3(unsigned(p.part_rows)), dim3(128), 0, s, p);
-  return st::launch_pdl(cond_combine<T, OWN, 1>, dim3(unsigned((p.part_rows + 3) / 4)), dim3(128), 0, s, p);
+  const bool four = p.part_rows <= (long long)st::device_sms() * 8;
+  const long long blocks = four ? p.part_rows : (p.part_rows + 3) / 4;
+  const int sms = st::num_sms();
+  if (sms < st::device_sms() && blocks > sms * 8LL) {      // a budget: as many blocks as run at once
+    const auto kern = four ? cond_combine<T, OWN, 4, true> : cond_combine<T, OWN, 1, true>;
+    return st::launch_pdl(kern, dim3(unsigned(sms * 8)), dim3(128), 0, s, p);
+  }
+  const auto kern = four ? cond_combine<T, OWN, 4, false> : cond_combine<T, OWN, 1, false>;
+  return st::launch_pdl(kern, dim3(unsigned(blocks)), dim3(128), 0, s, p);
 }
 template <typename T> st_status combine(const CondParams &p, cudaStream_t s) {
   return p.own.k ? combine_own<T, true>(p, s) : combine_own<T, false>(p, s);

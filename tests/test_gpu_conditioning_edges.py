@@ -218,3 +218,60 @@ def test_fp32_two_level_strides(S, L, Lp, D):
             fn(big, *keys, out, lse, workspace=ws, desc=desc)
             check_attn(q, segs, logical(out), lse, what=fn.__name__)
             assert (out[..., ts:, :] == 7.0).all() and (out[..., C:] == 7.0).all()
+
+
+def time_of(f, n=3):
+    f()
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    for _ in range(n):
+        f()
+    b.record()
+    torch.cuda.synchronize()
+    return a.elapsed_time(b) / n
+
+
+def budgeted(sms, f):
+    st.st_set_sm_budget(sms)
+    try:
+        return f()
+    finally:
+        st.st_set_sm_budget(0)
+
+
+@pytest.mark.parametrize("D", [40, 72, 128])
+def test_fp32_within_the_budget(D):
+    """The fp32 kernel on a few SMs: the bits of the whole GPU's run, and not on more SMs than it was given (one
+    SM takes far longer than all)."""
+    B, S, H, L = 3, 700, 4, 200
+    q, k, v = rand(260, B, 1, S, H, D, dtype=F32), rand(261, B, L, H, D, dtype=F32), rand(262, B, L, H, D, dtype=F32)
+    n = torch.tensor([L, 0, 77], dtype=torch.int32)
+    o, lse, _ = run_cross(q, k, v, kv_len=n.cuda())
+    check_attn(q, [sets_of(k, v, n)], o, lse, what="whole")
+    for sms in (1, 5):
+        o2, lse2, _ = budgeted(sms, lambda: run_cross(q, k, v, kv_len=n.cuda()))
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    q, k, v = rand(263, 1, 1, 8192, 4, D, dtype=F32), rand(264, 1, L, 4, D, dtype=F32), rand(265, 1, L, 4, D, dtype=F32)
+    out = torch.empty_like(q)
+    def call():
+        st.st_attn_cross(q, k, v, out)
+    assert budgeted(1, lambda: time_of(call)) > 8 * time_of(call)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [72, 128])
+@pytest.mark.parametrize("B,H,Hkv", [(40, 4, 2), (200, 8, 4)])
+def test_combine_within_the_budget(dtype, D, B, H, Hkv):
+    """Rows of split keys with own keys, joined by a few blocks (a warp and four warps a row): the same bits."""
+    Lp, L = 900, 40
+    n = torch.randint(0, L + 1, (B,), generator=torch.Generator().manual_seed(270)).int()
+    q = rand(271, B, 1, 1, H, D, dtype=dtype)
+    kp, vp = rand(272, 1, Lp, Hkv, D, dtype=dtype), rand(273, 1, Lp, Hkv, D, dtype=dtype)
+    k, v = rand(274, B, L, Hkv, D, dtype=dtype), rand(275, B, L, Hkv, D, dtype=dtype)
+    o, lse, ws = run_prefix(q, kp, vp, k, v, kv_len=n.cuda())
+    assert ws > 0
+    check_attn(q, [sets_of(kp, vp), sets_of(k, v, n)], o, lse, what="whole")
+    for sms in (1, 3):
+        for _ in range(3):
+            o2, lse2, _ = budgeted(sms, lambda: run_prefix(q, kp, vp, k, v, kv_len=n.cuda()))
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
