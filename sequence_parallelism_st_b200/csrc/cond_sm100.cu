@@ -652,8 +652,22 @@ __device__ __forceinline__ int q_tiles(bool spread, int n_qt, int n_kv) {
 }
 // Its n-th Q tile's slot where each tile has its own.
 __device__ __forceinline__ int own_slot(bool spread, int X, uint32_t n) { return spread ? X : 2 * X + int(n & 1); }
-// TIGHT: slot `i` of the Q tiles after slot q0.
-__device__ __forceinline__ int q_slot(int q0, int i, int nq) { return q0 + i >= nq ? q0 + i - nq : q0 + i; }
+// TIGHT: the next slot of the Q tiles, which take the slots in turn, and the
+// parity of its turn.  A slot has its own barrier then: it cannot be filled again
+// before its tile has been released, so no waiter falls behind by two phases (a
+// tile's barriers in turn could, where others' rows left it one tile in a slot
+// after another).
+struct QTurn {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ QTurn ahead(int i, int nq) const {
+    QTurn t;
+    const bool wrap = slot + i >= nq;
+    t.slot = slot + i - (wrap ? nq : 0);
+    t.parity = parity ^ (wrap ? 1 : 0);
+    return t;
+  }
+};
 
 template <int D, bool MIX>
 __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
@@ -669,7 +683,7 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
   int2 *sSet = reinterpret_cast<int2 *>(sQ + K::ROOM);
   Item *sItem = reinterpret_cast<Item *>(sSet + 2 * K::TABLE);
   uint64_t *bars = reinterpret_cast<uint64_t *>(sItem + ITEMS);
-  uint64_t *q_full = bars, *q_empty = q_full + NQ;   // q_full: two per tile, its Q tiles in turn; q_empty: by slot
+  uint64_t *q_full = bars, *q_empty = q_full + NQ;   // q_empty: by slot; q_full: the same (TIGHT), or two per tile, its Q tiles in turn
   uint64_t *k_full = q_empty + NQ, *k_empty = k_full + NB;      // k_empty, v_empty: one arrival per tile that reads the stage
   uint64_t *v_full = k_empty + NB, *v_empty = v_full + NB, *v_ready = v_empty + NB;
   // per tile: S ready; P written; O of an item complete
@@ -764,8 +778,7 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
         bool first = true;
         Walk<D> wk(a, sSet);
         const bool tight = K::TIGHT && nq < NQ;
-        int q0 = 0;                                   // next Q slot
-        uint32_t q_phase = 1;                         // parity its release shows
+        QTurn qt;                                     // TIGHT: next Q slot
         // the item's Q tiles [i0, i1)
         auto load_q = [&](const Item &it, int i0, int i1) -> bool {
           i1 = min(i1, q_tiles(spread, it.n_qt, it.n_kv));
@@ -773,16 +786,13 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
           for (int i = i0; i < i1; ++i) {
             const int X = spread ? int((ring.pos + i) % NT) : i;
             const uint32_t n = qn >> 2 * X & 3;
-            uint64_t *full = q_full + 2 * X + (n & 1);
-            const int slot = K::TIGHT ? q0 : own_slot(spread, X, n);
-            const uint32_t ph = K::TIGHT ? q_phase : ((spread ? n : n >> 1) & 1) ^ 1;
+            const int slot = K::TIGHT ? qt.slot : own_slot(spread, X, n);
+            uint64_t *full = q_full + (K::TIGHT ? slot : 2 * X + int(n & 1));
+            const uint32_t ph = (K::TIGHT ? qt.parity : (spread ? n : n >> 1) & 1) ^ 1;
             if (!(ok = mbar_wait(q_empty + slot, ph, epoch))) return false;
             qn ^= (n ^ ((n + 1) & 3)) << 2 * X;
             uint8_t *dst = sQ + slot * K::QTILE;
-            if (K::TIGHT && ++q0 == nq) {
-              q0 = 0;
-              q_phase ^= 1;
-            }
+            if (K::TIGHT) qt = qt.ahead(1, nq);
             const int row = it.r0 + (spread ? 0 : X * a.tile_rows);
             mbar_expect_tx(full, a.tile_rows * (K::SW0 + K::SW1));
             if (a.c.G > 1) {
@@ -884,11 +894,16 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
             for (int i = last_kv; i >= 0 && i > last_kv - NB; --i) mbar_drain(k_full + i % NB, (i / NB) & 1);
             for (int i = last_kv; i >= 0 && i > last_kv - NB; --i) mbar_drain(v_full + i % NB, (i / NB) & 1);
           }
-          for (int X = 0; X < NT; ++X)
-            for (uint32_t k = 1; k <= 2; ++k) {       // (a barrier never used answers at once)
-              const uint32_t n = ((qn >> 2 * X) - k) & 3;
-              mbar_drain(q_full + 2 * X + (n & 1), n >> 1);
-            }
+          // (a barrier never used answers at once)
+          if (K::TIGHT) {
+            for (int i = 0; i < nq; ++i) mbar_drain(q_full + i, qt.parity ^ (i < qt.slot ? 0 : 1));
+          } else {
+            for (int X = 0; X < NT; ++X)
+              for (uint32_t k = 1; k <= 2; ++k) {
+                const uint32_t n = ((qn >> 2 * X) - k) & 3;
+                mbar_drain(q_full + 2 * X + (n & 1), n >> 1);
+              }
+          }
         }
       }
       __syncwarp();
@@ -905,7 +920,7 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
       Ring<NB> ring;
       Reader rd;
       uint32_t qc = 0, steps = 0;                      // Q tiles and steps of this tile so far
-      int q0 = 0;                                      // first Q slot of the item
+      QTurn qt;                                        // TIGHT: first Q slot of the item
       // This tile has waited for the stages it now holds (resident: those of its
       // run).  The run's first item may have no rows for it, so a later one waits;
       // the stages' phases stay until this tile, too, has handed them back.
@@ -940,9 +955,11 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
         const int j0 = first_step<NT>(spread, ring.pos, X), inc = spread ? NT : 1;
         const bool here = X < cur.n_qt && j0 < cur.n;
         if (here) {
-          const int slot = K::TIGHT ? q_slot(q0, q_index(spread, j0, X), nq) : own_slot(spread, X, qc);
+          const QTurn mine = qt.ahead(q_index(spread, j0, X), nq);
+          const int slot = K::TIGHT ? mine.slot : own_slot(spread, X, qc);
           const uint32_t qa = sdesc_lo<16>(aQ + slot * K::QTILE);
-          if (!(ok = mbar_wait(q_full + 2 * X + (qc & 1), (qc >> 1) & 1, epoch))) break;
+          if (!(ok = mbar_wait(q_full + (K::TIGHT ? slot : 2 * X + int(qc & 1)), K::TIGHT ? mine.parity : (qc >> 1) & 1, epoch)))
+            break;
           ++qc;
           for (int j = j0; j < cur.n; j += inc, ++steps) {
             // S(j), over P(j - 1), which PV(j - 1) has read by then; only as many
@@ -1003,7 +1020,7 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
             tc_commit(lead, v_empty + bar);
           }
         }
-        if (K::TIGHT) q0 = q_slot(q0, q_tiles(spread, cur.n_qt, cur.n), nq);
+        if (K::TIGHT) qt = qt.ahead(q_tiles(spread, cur.n_qt, cur.n), nq);
         if (resident) ring.run += cur.release;
         else ring.pos += cur.n;
         if (!here && ok) ok = fetch();
@@ -1093,7 +1110,8 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
     const f32x2 scale2 = pair(sl2, sl2);
     uint32_t gs = 0, oc = 0, pos = 0;          // steps and items of this tile; steps of all
     const int inc = spread ? NT : 1;
-    int q0 = 0, slot = 0;                      // Q slots: the item's first, this tile's last
+    QTurn qt;                                  // TIGHT: the item's first Q slot
+    int slot = 0;                              // this tile's last
     bool pending = false;                      // O of the item before is on its way out of its Q slot
     // Hands that slot to the loader once the store has read it.
     auto release_slot = [&]() {
@@ -1112,8 +1130,8 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
       const int n_kv = it.n_kv, n0 = it.n0, n1 = it.n1, s0 = it.s0, j0 = it.j0;
       if (it.n_qt == 0) break;
       const int first = first_step<NT>(spread, pos, X);
-      const int mine = K::TIGHT ? q_slot(q0, q_index(spread, first, X), nq) : own_slot(spread, X, oc);
-      if (K::TIGHT) q0 = q_slot(q0, q_tiles(spread, it.n_qt, n_kv), nq);
+      const int mine = K::TIGHT ? qt.ahead(q_index(spread, first, X), nq).slot : own_slot(spread, X, oc);
+      if (K::TIGHT) qt = qt.ahead(q_tiles(spread, it.n_qt, n_kv), nq);
       pos += n_kv;
       if (X >= it.n_qt || first >= n_kv) release_slot();   // (no first step to do it at)
       if (X >= it.n_qt) {

@@ -275,3 +275,24 @@ def test_combine_within_the_budget(dtype, D, B, H, Hkv):
         for _ in range(3):
             o2, lse2, _ = budgeted(sms, lambda: run_prefix(q, kp, vp, k, v, kv_len=n.cuda()))
             assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("D", [72, 128])
+@pytest.mark.parametrize("S", [100, 333])
+@pytest.mark.parametrize("L", [2, 200])
+def test_items_of_one_tile_with_kept_keys(D, S, L):
+    """Row after row of queries with one set of keys and nothing to load but Q: at head dim 128 the loader runs up to
+    four items ahead of a row tile, whose waits must all end (many short launches, items of one and two tiles)."""
+    B, T, H, Hkv = 2, 3, 5, 1
+    q = rand(280, B, T, S + 3, H, D)[:, :, :S]
+    k, v = rand(281, B, L, Hkv, D), rand(282, B, L, Hkv, D)
+    o, lse = torch.zeros(B, T, S + 3, H, D, dtype=BF, device="cuda")[:, :, :S], torch.empty(B, T, H, S, device="cuda")
+    st.st_attn_cross(q, k, v, o, lse)
+    assert st.st_check_device_status() == st.ST_OK
+    check_attn(q, [sets_of(k, v)], o, lse, what="whole")
+    for sms in (1, 3, 7, 11):
+        o2, lse2 = torch.zeros(B, T, S + 3, H, D, dtype=BF, device="cuda")[:, :, :S], torch.empty_like(lse)
+        for _ in range(100):
+            budgeted(sms, lambda: st.st_attn_cross(q, k, v, o2, lse2))
+        assert st.st_check_device_status() == st.ST_OK
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
