@@ -68,7 +68,7 @@ struct CondParams {
   int G;                       // heads packed into the rows (H / H_kv), or 1
   int HW;                      // heads walked: H / G
   int hdiv;                    // kv head = walked head / hdiv
-  int T0, S0, B0;              // the call's sizes
+  int T0, S0;                  // frames and queries of the call
   KvSeg seg[2];
   int n_seg;
   KvSeg own;                   // attended by the combine kernel (packed batches); own.k NULL: none

@@ -124,7 +124,6 @@ st_status make_plan(const st_attn_desc *desc, const st_kv_desc *d0, const st_kv_
   }
   p.T0 = g.T;
   p.S0 = g.S;
-  p.B0 = g.B;
   p.bm = 1;
   // one stride between all rows of a batch
   const bool flat = tokens && (g.T == 1 || (g.st == (long long)g.S * g.ss &&
