@@ -733,6 +733,15 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
       prefetch_map(&mp.v[0]);
     }
   }
+  // the rows behind the whole groups of a tile are 0, and their scores as tame as
+  // the others' (left as they were they could be NaN and have O rescaled in every step)
+  if (a.tile_rows < BLOCK_M) {
+    for (int i = a.tile_rows * K::SW0 + 16 * int(threadIdx.x); i < K::QT0; i += 16 * K::THREADS)
+      for (int n = 0; n < nq; ++n) *reinterpret_cast<uint4 *>(sQ + n * K::QTILE + i) = make_uint4(0, 0, 0, 0);
+    for (int i = K::QT0 + a.tile_rows * K::SW1 + 16 * int(threadIdx.x); i < K::QTILE; i += 16 * K::THREADS)
+      for (int n = 0; n < nq; ++n) *reinterpret_cast<uint4 *>(sQ + n * K::QTILE + i) = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+  }
   // barriers and TMEM are set up: let the next kernel of the stream be
   // scheduled, then wait for the previous one before any global access
   pdl_trigger();
@@ -1177,15 +1186,14 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
           for (int e = 0; e < 4; ++e)
             mxp[e] = fmax3(mxp[e], __uint_as_float(sr[c >> 1][(c & 1) * 8 + 2 * e]),
                            __uint_as_float(sr[c >> 1][(c & 1) * 8 + 2 * e + 1]));
-        // A step without any key leaves the row at NO_KEY: its weights are 0.  A
-        // score that is NaN or +inf makes the maximum NaN (inf * 0 is NaN), and with
-        // it the weights of the row, its sum and its O, now and in later steps.
-        float mx = fmax2(fmax2(fmax3(mxp[0], mxp[1], mxp[2]), mxp[3]) * sl2, NO_KEY);
-        mx = fmaf(mx, 0.f, mx);
+        // A step without any key leaves the row at NO_KEY: its weights are 0.  A NaN
+        // score makes the maximum NaN from here on; one of +inf stays the maximum.
+        // Either makes the row NaN where O is written.
+        const float mx = fmax2(fmax2(fmax3(mxp[0], mxp[1], mxp[2]), mxp[3]) * sl2, NO_KEY);
         if (j == first) {
           m = mx;
         } else {
-          const bool need = !(mx <= m + 8.0f) && m == m;
+          const bool need = !(mx <= m + 8.0f);         // (in every step of a NaN row; the test of m for it cost 1.5%)
           if (__any_sync(0xffffffffu, need)) {
             // S(j) complete means PV(j - 1) is (one thread issued both): rescale O in TMEM
             const float corr = need ? ex2_mufu(m - mx) : 1.0f;
@@ -1269,8 +1277,9 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
         l = __uint_as_float(sum[0]);
       }
       if (some && m != NO_KEY) {               // else no key counted: o = 0, lse = -inf
-        inv = __fdividef(1.0f, l);
-        lse = (m + __log2f(l)) * 0.6931471805599453f;
+        const float bad = m - m;               // NaN for a maximum of NaN or +inf, else 0
+        inv = __fdividef(1.0f, l) + bad;
+        lse = (m + __log2f(l)) * 0.6931471805599453f + bad;
       }
       const f32x2 inv2 = pair(inv, inv);
       if (tma) {
