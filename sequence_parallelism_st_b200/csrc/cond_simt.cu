@@ -9,10 +9,13 @@
 // tile in shared memory, so two CTAs fit an SM at head dim 128 and one loads
 // while the other multiplies.
 //
-// Bound by the pieces of shared memory that feed 4 x 4 products a thread: 16,384
-// rows x 16 heads, 512 keys of 128 channels 27 TFLOP/s, 300 of 72 channels 17.5 (a
-// second 64-channel piece holds 8).  Asynchronous copies of the next K and V tile
-// under the products were no faster.
+// Bound by the pieces of shared memory that feed 4 x 4 products a thread (72
+// channels: issue slots 61%, shared memory 44%, FMA pipe 40%): 16,384 rows x 16
+// heads, 512 keys of 128 channels 2531 us (27 TFLOP/s), 300 of 72 channels 1293 us
+// (17.5; a second 64-channel piece holds 8).  Asynchronous copies of the next K and
+// V tile under the products were no faster.  A tile of fewer rows costs what 64 do:
+// one query of 24 heads on 8, 2 x 20,736 keys of 128 channels 439 us, of 52 us that
+// reading K and V takes.
 #include <math.h>
 
 #include "cond.cuh"

@@ -15,7 +15,7 @@
 // pipe 32%, special-function unit 39% busy at 320 keys).  Second comes the
 // instruction cache: all roles together are 60 to 85 KB of code, and every
 // variant that shortened them got faster (16 heads x 72, 65,536 rows, 320 keys:
-// 176 us at 84 KB, 161 us at 71 KB).
+// 176 us at 84 KB, 161 us at 71 KB, where it still is).
 //
 // Design (one persistent CTA per SM, warp-specialised):
 //   * A work item is up to NT tiles of 128 rows of one (unit, head): three for
@@ -45,12 +45,13 @@
 //   * Every wait is bounded; a wait that runs out sets an error word and an
 //     abort epoch, in-flight copies are drained, TMEM is freed.
 //
-// Measured (device time, 65,536 rows, 16 heads; the spatial kernel of this
-// library beside it needs 210 us for 256 keys of 72 channels):
-//   72 channels:  64 keys 89 us, 128 108 us, 320 156 us (618 TF/s), 1024 466 us
-//                 (663 TF/s), 4096 1607 us (770 TF/s)
-//   128 channels: 64 keys 147 us, 128 138 us, 320 316 us (540 TF/s), 1024 582 us
-//                 (944 TF/s), 4096 2040 us (1078 TF/s)
+// Measured (device time of short runs at 1.9 GHz, 65,536 rows, 16 heads; the spatial
+// kernel of this library beside it needs 213 us for 256 keys of 72 channels; under
+// the power cap, at 1.7 to 1.85 GHz, the long ones take 5 to 15% more):
+//   72 channels:  64 keys 87 us, 128 107 us, 320 160 us (604 TF/s), 1024 480 us
+//                 (644 TF/s), 4096 1631 us (758 TF/s)
+//   128 channels: 64 keys 137 us, 128 129 us, 320 290 us (592 TF/s), 1024 560 us
+//                 (981 TF/s), 4096 1928 us (1140 TF/s)
 #include <cuda.h>
 #include <math.h>
 #include <string.h>
@@ -114,7 +115,8 @@ template <int D, bool MIX = false> struct Cfg {
   // two chains out of step.  (TF/s over 4096 and 300 keys: 1078 and 522 so; 2 K and
   // 1 V 955 and 532; K and V in turn in three tiles 874 and 556; O staged apart
   // from one Q tile each, the chains in step, 886 and 528, with row tile 1 held
-  // back by 2 steps 924 and 505.)
+  // back by 2 steps 924 and 505.  With a barrier per Q slot the kept form is at 1140
+  // and 544.)
   static constexpr int NQ = 2 * NT;
   static constexpr bool TIGHT = D == 128;
   static constexpr bool DENSE = D == 72 || D == 80;
@@ -1230,6 +1232,9 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
               w.y = ex2_mufu(w.y);
             }
             if (!K::ONES) acc[e & 1] = fadd2(acc[e & 1], pair(w.x, w.y));
+            // rounded to bf16, the operand of PV (tf32 would halve its rate and double P
+            // in TMEM): at most 2^-8 relative, so O is off by at most 2^-8 of the weighted
+            // mean of |V| (measured, with O's own rounding: 0.0023 relative, 0.0017 without)
             pk[e] = st::pack_bf16x2(w.x, w.y);
           }
           COND_ST8(tS + c * 8, pk);
@@ -1278,6 +1283,8 @@ __global__ void __launch_bounds__(Cfg<D, MIX>::THREADS, 1)
       }
       if (some && m != NO_KEY) {               // else no key counted: o = 0, lse = -inf
         const float bad = m - m;               // NaN for a maximum of NaN or +inf, else 0
+        // (the fast forms: l is at least 1 and below 2^39, where they are off by 2 units and
+        // by 2 units or 2^-21.4, far below the weights' rounding)
         inv = __fdividef(1.0f, l) + bad;
         lse = (m + __log2f(l)) * 0.6931471805599453f + bad;
       }

@@ -12,9 +12,11 @@
 // of two to four such groups; a warp has the loads of its next task in flight while
 // it works on one, and the sums of a task's groups run side by side.  Gains lie
 // in shared memory; the arithmetic is in pairs, since issue slots are what is
-// short next (75% used).  bf16: 24 + 24 heads of 128 channels, 65,536 tokens 289 us
-// (5.7 TB/s; 394 us without the loads ahead and the pairs), 16 + 16 heads of 72
-// (27 of 32 lanes at work), 19,200 tokens 40 us (4.5 TB/s; 69 us).
+// short next (75% used).  bf16: 24 + 24 heads of 128 channels, 65,536 tokens 299 us
+// in short runs (5.5 TB/s; 334 us under the power cap at 1.78 GHz; 394 us without the
+// loads ahead and the pairs), 16 + 16 heads of 72 (27 of 32 lanes at work), 19,200
+// tokens 42 us (4.2 TB/s; 69 us).  fp32: 535 to 545 us (6.0 TB/s) and 64 to 67 us
+// (5.4 TB/s).
 #include "common.cuh"
 
 namespace {
@@ -265,7 +267,7 @@ template <typename T, bool HALVES, bool ROPE, int UNROLL> st_status launch_group
   }
 }
 // Four groups of bf16 a task, or three where that leaves fewer places empty
-// (48 heads of 128 channels: 289 us with four, 309 with three; 20 heads of 64,
+// (65,536 tokens, 48 heads of 128 channels: 289 us with four, 309 with three, in one run; 20 heads of 64,
 // five groups: 77 and 67); two of fp32 (four spill).
 template <typename T, bool HALVES, bool ROPE> st_status launch_pairing(QkArgs a, cudaStream_t s) {
   const int hpw = 32 / (a.D / 8), groups = (a.heads + hpw - 1) / hpw;
